@@ -28,6 +28,7 @@ SUM, MEAN = 0, 1
 BF16, FP32 = 0, 1
 ACCUMULATE_DHIDDEN, ACCUMULATE_DWEIGHT = 1, 2
 DHIDDEN_BF16, DWEIGHT_BF16 = 4, 8
+MAX_TOP_K = 32
 
 # flce_option values (include/flce.h)
 OPTIONS = {
@@ -53,6 +54,13 @@ SIGNATURES = {
     "flce_backward_ex": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,
                                  c_i32, c_i32, c_vp, c_f32, c_i64, c_vp, c_vp, c_vp, c_i32, c_vp,
                                  c_size, c_vp]),
+    "flce_logprobs_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i32, c_i32]),
+    "flce_logprobs_forward": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32, c_f64,
+                                      c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size,
+                                      c_vp]),
+    "flce_logprobs_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64,
+                                       c_f32, c_f64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                       c_size, c_vp]),
     "flce_set_option": (c_i32, [c_i32, c_i64]),
     "flce_get_option": (c_i32, [c_i32, ctypes.POINTER(c_i64)]),
     "flce_forward_noalloc": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,

@@ -34,7 +34,7 @@
 #include <vector>
 
 #include "../../include/flce.h"
-#include "small_kernels.cuh"
+#include "logprob_kernels.cuh"
 
 namespace flce {
 namespace {
@@ -499,7 +499,9 @@ cudaError_t run_gemm_cg(DevInfo* d, int kind, const GemmProblem& p0,
     g1.m_tiles = g1.n_tiles = 0;
   }
   const GemmProblem& q1 = p1 ? *p1 : p0;
-  const int tiles = g0.m_tiles * g0.n_tiles + g1.m_tiles * g1.n_tiles;
+  // what is handed out: tiles, or runs of run_n column tiles
+  const int tiles = Epi::kRun ? g0.m_tiles * ((g0.n_tiles + g0.run_n - 1) / g0.run_n)
+                              : g0.m_tiles * g0.n_tiles + g1.m_tiles * g1.n_tiles;
   const int units = std::max(1, std::min(tiles, d->sms / kCG));
   if (ctas_out != nullptr) *ctas_out = units * kCG;
   cudaLaunchConfig_t cfg = {};
@@ -713,12 +715,14 @@ flce_status forward_fp32(DevInfo* d, const void* hidden, const void* weight,
 }
 
 // ---------------------------------------------------------------- backward
+// rg (scoring operator): per-row upstream gradients instead of the loss's scalar.
 flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const void* weight,
                           const int64_t* labels, const float* lse, int64_t N, int64_t H,
                           int64_t V, int64_t ignore_index, float softcap, int32_t reduction,
                           const float* grad_output, float grad_scale, const long long* n_valid,
                           bool n_valid_is_count, float* d_hidden, float* d_weight,
-                          int32_t flags, void* ws, cudaStream_t st) {
+                          int32_t flags, void* ws, cudaStream_t st,
+                          const RowGrads* rg = nullptr) {
   const bool acc_dh = (flags & FLCE_ACCUMULATE_DHIDDEN) != 0;
   const bool acc_dw = (flags & FLCE_ACCUMULATE_DWEIGHT) != 0;
   const bool want_dh = d_hidden != nullptr;  // a NULL output is not computed
@@ -902,16 +906,30 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
       }
       cudaError_t e;
       const GemmProblem pz{&t_hid_k, &t_w_k, &t_g_store, rows, cols, gz};
-      if (softcap > 0.f) {
-        DzEpi<true>::Params ep{lab,  lsev,    ignore_index, static_cast<int>(t0),
-                               rows, static_cast<int>(v0), cols, softcap, 1.0f / softcap,
-                               resid, V};
-        e = run_gemm<DzEpi<true>, false, false>(d, o, dz_bn, kBwdDz, pz, ep, nullptr, ep, st);
-      } else {
-        DzEpi<false>::Params ep{lab,  lsev, ignore_index, static_cast<int>(t0), rows,
-                                static_cast<int>(v0), cols, 0.f, 0.f, resid, V};
-        e = run_gemm<DzEpi<false>, false, false>(d, o, dz_bn, kBwdDz, pz, ep, nullptr, ep, st);
-      }
+      const auto dz = [&](auto epi) {
+        using Epi = decltype(epi);
+        typename Epi::Params ep{lab,
+                                lsev,
+                                ignore_index,
+                                static_cast<int>(t0),
+                                rows,
+                                static_cast<int>(v0),
+                                cols,
+                                softcap,
+                                softcap > 0.f ? 1.0f / softcap : 0.f,
+                                resid,
+                                V,
+                                rg ? rg->d_logprobs : nullptr,
+                                rg ? rg->d_entropy : nullptr,
+                                rg ? rg->entropy : nullptr,
+                                perm,
+                                rg ? rg->inv_temp : 1.0f};
+        return run_gemm<Epi, false, false>(d, o, dz_bn, kBwdDz, pz, ep, nullptr, ep, st);
+      };
+      if (rg != nullptr)
+        e = softcap > 0.f ? dz(DzEpi<true, true>{}) : dz(DzEpi<false, true>{});
+      else
+        e = softcap > 0.f ? dz(DzEpi<true>{}) : dz(DzEpi<false>{});
       if (e != cudaSuccess) return cuda_fail(e);
 
       // 2) dHidden[t0:t0+rows] (+)= dZ . W[v0:v0+cols]
@@ -1019,7 +1037,8 @@ flce_status backward_fp32(DevInfo* d, const void* hidden, const void* weight,
                           const int64_t* labels, const float* lse, int64_t N, int64_t H,
                           int64_t V, int64_t ignore_index, float softcap, int32_t reduction,
                           const float* grad_output, float grad_scale, const long long* n_valid,
-                          float* d_hidden, float* d_weight, int32_t flags, cudaStream_t st) {
+                          float* d_hidden, float* d_weight, int32_t flags, cudaStream_t st,
+                          const RowGrads* rg = nullptr) {
   const int acc_dh = (flags & FLCE_ACCUMULATE_DHIDDEN) ? 1 : 0;
   const int acc_dw = (flags & FLCE_ACCUMULATE_DWEIGHT) ? 1 : 0;
   const int n = static_cast<int>(N), h = static_cast<int>(H), v = static_cast<int>(V);
@@ -1027,30 +1046,132 @@ flce_status backward_fp32(DevInfo* d, const void* hidden, const void* weight,
   const size_t sh_dh = (2 * static_cast<size_t>(h) + kSimtChunk) * sizeof(float);
   const size_t sh_dw = (2 * static_cast<size_t>(h) + kSimtThreads) * sizeof(float);
   (void)d;
-  cudaError_t e = set_smem_attr(simt_dh_kernel, 2 * kSimtMaxH * 4 + kSimtChunk * 4);
+  const auto dh_kernel = rg ? simt_dh_kernel<true> : simt_dh_kernel<false>;
+  const auto dw_kernel = rg ? simt_dw_kernel<true> : simt_dw_kernel<false>;
+  const RowGrads rows = rg ? *rg : RowGrads{};
+  cudaError_t e = set_smem_attr(dh_kernel, 2 * kSimtMaxH * 4 + kSimtChunk * 4);
   if (e != cudaSuccess) return cuda_fail(e);
-  e = set_smem_attr(simt_dw_kernel, 2 * kSimtMaxH * 4 + kSimtThreads * 4);
+  e = set_smem_attr(dw_kernel, 2 * kSimtMaxH * 4 + kSimtThreads * 4);
   if (e != cudaSuccess) return cuda_fail(e);
   if (n > 0 && d_hidden != nullptr) {
     e = launch(kSimt, st, [&] {
-      simt_dh_kernel<<<n, kSimtThreads, sh_dh, st>>>(
+      dh_kernel<<<n, kSimtThreads, sh_dh, st>>>(
           static_cast<const float*>(hidden), static_cast<const float*>(weight), labels, lse, n, h,
-          v, ignore_index, softcap, grad_output, grad_scale, n_valid, mean, acc_dh, d_hidden);
+          v, ignore_index, softcap, grad_output, grad_scale, n_valid, mean, acc_dh, d_hidden,
+          rows);
     });
     if (e != cudaSuccess) return cuda_fail(e);
   }
   if (d_weight == nullptr) return FLCE_OK;
   e = launch(kSimt, st, [&] {
-    simt_dw_kernel<<<v, kSimtThreads, sh_dw, st>>>(
+    dw_kernel<<<v, kSimtThreads, sh_dw, st>>>(
         static_cast<const float*>(hidden), static_cast<const float*>(weight), labels, lse, n, h, v,
-        ignore_index, softcap, grad_output, grad_scale, n_valid, mean, acc_dw, d_weight);
+        ignore_index, softcap, grad_output, grad_scale, n_valid, mean, acc_dw, d_weight, rows);
   });
   if (e != cudaSuccess) return cuda_fail(e);
   return FLCE_OK;
 }
 
+// The body of flce_backward_ex and, with rg, of flce_logprobs_backward.
+flce_status backward_any(const void* hidden, const void* weight, const int64_t* labels,
+                         const float* lse, int64_t N, int64_t H, int64_t V, int64_t ignore_index,
+                         float softcap, int32_t reduction, int32_t dtype,
+                         const float* grad_output, float grad_scale, int64_t num_label_tokens,
+                         const int64_t* num_valid, float* d_hidden, float* d_weight,
+                         int32_t flags, void* workspace, size_t workspace_bytes, void* stream,
+                         const RowGrads* rg) {
+  if ((flags & ~kAllBwdFlags) != 0) return FLCE_ERR_ARG;
+  const Opts o = opts();
+  flce_status s = check_common(o, hidden, weight, labels, N, H, V, softcap, reduction, dtype,
+                               workspace, workspace_bytes);
+  if (s != FLCE_OK) return s;
+  const GradScratch gs = grad_scratch(o, N, H, V, dtype == FLCE_BF16, flags);
+  if (workspace_bytes < gs.end) return FLCE_ERR_WORKSPACE;
+  // a NULL d_hidden or d_weight is not computed; one of them must be given
+  if ((d_hidden == nullptr && d_weight == nullptr) || (N > 0 && lse == nullptr))
+    return FLCE_ERR_ARG;
+  if (!aligned16(d_hidden) || !aligned16(d_weight)) return FLCE_ERR_ARG;
+  if (!(grad_scale == grad_scale) || grad_scale == INFINITY || grad_scale == -INFINITY)
+    return FLCE_ERR_ARG;
+  // the gradient of a 'sum' loss normalised by max(num_label_tokens, 1)
+  const float gscale =
+      static_cast<float>(static_cast<double>(grad_scale) /
+                         label_token_divisor(reduction, num_label_tokens));
+  DevInfo* d = nullptr;
+  s = device_info(&d);
+  if (s != FLCE_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), st);  // status word
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (N == 0) {
+    if (d_weight == nullptr || (flags & FLCE_ACCUMULATE_DWEIGHT)) return FLCE_OK;  // adds nothing
+    const size_t elem = (flags & FLCE_DWEIGHT_BF16) ? 2 : sizeof(float);  // +0.0 in both
+    e = cudaMemsetAsync(d_weight, 0, static_cast<size_t>(V) * H * elem, st);
+    return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
+  }
+  // bf16 outputs: the gradient is computed into fp32 scratch (overwritten, not
+  // accumulated) and rounded once into the caller's buffer afterwards.
+  char* wsb = static_cast<char*>(workspace);
+  float* dh32 = (d_hidden != nullptr && (flags & FLCE_DHIDDEN_BF16))
+                    ? reinterpret_cast<float*>(wsb + gs.dh) : d_hidden;
+  float* dw32 = (d_weight != nullptr && (flags & FLCE_DWEIGHT_BF16))
+                    ? reinterpret_cast<float*>(wsb + gs.dw) : d_weight;
+  int32_t inner = flags & (FLCE_ACCUMULATE_DHIDDEN | FLCE_ACCUMULATE_DWEIGHT);
+  if (flags & FLCE_DHIDDEN_BF16) inner &= ~FLCE_ACCUMULATE_DHIDDEN;
+  if (flags & FLCE_DWEIGHT_BF16) inner &= ~FLCE_ACCUMULATE_DWEIGHT;
+  const bool compacts = (dtype == FLCE_BF16 && o.compact);
+  if (!compacts) {  // the compaction checks the labels itself
+    e = launch(kHelper, st, [&] {
+      label_range_kernel<<<static_cast<unsigned>((N + 255) / 256), 256, 0, st>>>(
+          labels, static_cast<int>(N), ignore_index, V, ws_status(workspace));
+    });
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  const long long* nv = reinterpret_cast<const long long*>(num_valid);
+  const bool own_count = (nv == nullptr);
+  if (nv == nullptr && !compacts && rg == nullptr) {
+    long long* out = ws_nvalid(workspace);
+    e = launch(kHelper, st, [&] {
+      count_valid_kernel<<<1, kFinalThreads, 0, st>>>(labels, static_cast<int>(N), ignore_index,
+                                                      V, out);
+    });
+    if (e != cudaSuccess) return cuda_fail(e);
+    nv = out;
+  }
+  if (dtype == FLCE_BF16)
+    s = backward_bf16(d, o, hidden, weight, labels, lse, N, H, V, ignore_index, softcap,
+                      reduction, grad_output, gscale, nv, own_count, dh32, dw32, inner, workspace,
+                      st, rg);
+  else
+    s = backward_fp32(d, hidden, weight, labels, lse, N, H, V, ignore_index, softcap, reduction,
+                      grad_output, gscale, nv, dh32, dw32, inner, st, rg);
+  if (s != FLCE_OK) return s;
+  const struct {
+    int32_t flag, acc;
+    const float* src;
+    void* dst;
+    size_t n;
+  } outs[2] = {{FLCE_DHIDDEN_BF16, FLCE_ACCUMULATE_DHIDDEN, dh32, d_hidden,
+                static_cast<size_t>(N) * H},
+               {FLCE_DWEIGHT_BF16, FLCE_ACCUMULATE_DWEIGHT, dw32, d_weight,
+                static_cast<size_t>(V) * H}};
+  for (const auto& out : outs) {
+    if (!(flags & out.flag) || out.dst == nullptr) continue;
+    const unsigned blocks = static_cast<unsigned>(
+        std::min<size_t>((out.n / 8 + 255) / 256 + 1, static_cast<size_t>(d->sms) * 8));
+    e = launch(kHelper, st, [&] {
+      f32_to_bf16_kernel<<<blocks, 256, 0, st>>>(out.src, static_cast<__nv_bfloat16*>(out.dst),
+                                                 out.n, (flags & out.acc) ? 1 : 0);
+    });
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return FLCE_OK;
+}
+
 }  // namespace
 }  // namespace flce
+
+#include "logprobs_api.cuh"
 
 using namespace flce;
 
@@ -1138,92 +1259,9 @@ flce_status flce_backward_ex(const void* hidden, const void* weight, const int64
                              int64_t num_label_tokens, const int64_t* num_valid,
                              float* d_hidden, float* d_weight, int32_t flags, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  if ((flags & ~kAllBwdFlags) != 0) return FLCE_ERR_ARG;
-  const Opts o = opts();
-  flce_status s = check_common(o, hidden, weight, labels, N, H, V, softcap, reduction, dtype,
-                               workspace, workspace_bytes);
-  if (s != FLCE_OK) return s;
-  const GradScratch gs = grad_scratch(o, N, H, V, dtype == FLCE_BF16, flags);
-  if (workspace_bytes < gs.end) return FLCE_ERR_WORKSPACE;
-  // a NULL d_hidden or d_weight is not computed; one of them must be given
-  if ((d_hidden == nullptr && d_weight == nullptr) || (N > 0 && lse == nullptr))
-    return FLCE_ERR_ARG;
-  if (!aligned16(d_hidden) || !aligned16(d_weight)) return FLCE_ERR_ARG;
-  if (!(grad_scale == grad_scale) || grad_scale == INFINITY || grad_scale == -INFINITY)
-    return FLCE_ERR_ARG;
-  // the gradient of a 'sum' loss normalised by max(num_label_tokens, 1)
-  const float gscale =
-      static_cast<float>(static_cast<double>(grad_scale) /
-                         label_token_divisor(reduction, num_label_tokens));
-  DevInfo* d = nullptr;
-  s = device_info(&d);
-  if (s != FLCE_OK) return s;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), st);  // status word
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (N == 0) {
-    if (d_weight == nullptr || (flags & FLCE_ACCUMULATE_DWEIGHT)) return FLCE_OK;  // adds nothing
-    const size_t elem = (flags & FLCE_DWEIGHT_BF16) ? 2 : sizeof(float);  // +0.0 in both
-    e = cudaMemsetAsync(d_weight, 0, static_cast<size_t>(V) * H * elem, st);
-    return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
-  }
-  // bf16 outputs: the gradient is computed into fp32 scratch (overwritten, not
-  // accumulated) and rounded once into the caller's buffer afterwards.
-  char* wsb = static_cast<char*>(workspace);
-  float* dh32 = (d_hidden != nullptr && (flags & FLCE_DHIDDEN_BF16))
-                    ? reinterpret_cast<float*>(wsb + gs.dh) : d_hidden;
-  float* dw32 = (d_weight != nullptr && (flags & FLCE_DWEIGHT_BF16))
-                    ? reinterpret_cast<float*>(wsb + gs.dw) : d_weight;
-  int32_t inner = flags & (FLCE_ACCUMULATE_DHIDDEN | FLCE_ACCUMULATE_DWEIGHT);
-  if (flags & FLCE_DHIDDEN_BF16) inner &= ~FLCE_ACCUMULATE_DHIDDEN;
-  if (flags & FLCE_DWEIGHT_BF16) inner &= ~FLCE_ACCUMULATE_DWEIGHT;
-  const bool compacts = (dtype == FLCE_BF16 && o.compact);
-  if (!compacts) {  // the compaction checks the labels itself
-    e = launch(kHelper, st, [&] {
-      label_range_kernel<<<static_cast<unsigned>((N + 255) / 256), 256, 0, st>>>(
-          labels, static_cast<int>(N), ignore_index, V, ws_status(workspace));
-    });
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  const long long* nv = reinterpret_cast<const long long*>(num_valid);
-  const bool own_count = (nv == nullptr);
-  if (nv == nullptr && !compacts) {
-    long long* out = ws_nvalid(workspace);
-    e = launch(kHelper, st, [&] {
-      count_valid_kernel<<<1, kFinalThreads, 0, st>>>(labels, static_cast<int>(N), ignore_index,
-                                                      V, out);
-    });
-    if (e != cudaSuccess) return cuda_fail(e);
-    nv = out;
-  }
-  if (dtype == FLCE_BF16)
-    s = backward_bf16(d, o, hidden, weight, labels, lse, N, H, V, ignore_index, softcap,
-                      reduction, grad_output, gscale, nv, own_count, dh32, dw32, inner, workspace,
-                      st);
-  else
-    s = backward_fp32(d, hidden, weight, labels, lse, N, H, V, ignore_index, softcap, reduction,
-                      grad_output, gscale, nv, dh32, dw32, inner, st);
-  if (s != FLCE_OK) return s;
-  const struct {
-    int32_t flag, acc;
-    const float* src;
-    void* dst;
-    size_t n;
-  } outs[2] = {{FLCE_DHIDDEN_BF16, FLCE_ACCUMULATE_DHIDDEN, dh32, d_hidden,
-                static_cast<size_t>(N) * H},
-               {FLCE_DWEIGHT_BF16, FLCE_ACCUMULATE_DWEIGHT, dw32, d_weight,
-                static_cast<size_t>(V) * H}};
-  for (const auto& out : outs) {
-    if (!(flags & out.flag) || out.dst == nullptr) continue;
-    const unsigned blocks = static_cast<unsigned>(
-        std::min<size_t>((out.n / 8 + 255) / 256 + 1, static_cast<size_t>(d->sms) * 8));
-    e = launch(kHelper, st, [&] {
-      f32_to_bf16_kernel<<<blocks, 256, 0, st>>>(out.src, static_cast<__nv_bfloat16*>(out.dst),
-                                                 out.n, (flags & out.acc) ? 1 : 0);
-    });
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  return FLCE_OK;
+  return backward_any(hidden, weight, labels, lse, N, H, V, ignore_index, softcap, reduction,
+                      dtype, grad_output, grad_scale, num_label_tokens, num_valid, d_hidden,
+                      d_weight, flags, workspace, workspace_bytes, stream, nullptr);
 }
 
 flce_status flce_set_option(int32_t option, int64_t value) {

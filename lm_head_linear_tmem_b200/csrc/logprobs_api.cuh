@@ -1,0 +1,329 @@
+// Host side of the LM head's scoring operator (flce_logprobs_* in
+// include/flce.h): workspace layout, choice of the schedule and launches.
+// Included by flce_api.cu, whose helpers it uses.
+//
+// forward, bf16:  [row compaction] -> tc_gemm<ScoreEpi> -> score_finish
+// forward, fp32:  score_simt -> score_finish
+// backward:       flce_backward's, with per-row upstream gradients
+#pragma once
+
+namespace flce {
+namespace {
+
+// The plan has to be known without a device (workspace sizes): SMs of a B200.
+constexpr int kPlanSms = 148;
+// A token batch of at most one 128-row tile reads the weight once whatever the
+// tile shape; single CTAs then spend half the tensor-core time of a pair on
+// the tile's empty rows.
+constexpr int kFewRows = BM;
+constexpr int kMaxRun = 16;
+
+struct ScorePlan {
+  int cta_group;   // 1: 128 x 256 tiles of single CTAs, 2: 256-row tiles of pairs
+  int bn;          // columns of a tile
+  int run;         // column tiles of a run
+  int slots;       // partial results per row
+  int K;           // list length (0: no alternatives)
+  bool compact;    // rows without a token are left out of the GEMM
+};
+
+// Runs are as long as an even spread over the SMs allows: of the run lengths up
+// to kMaxRun the one with the least time in units of tiles, ceil(runs / workers)
+// * run, and of equal ones the longest (fewest partial results).
+ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k) {
+  ScorePlan P{};
+  P.K = top_k > 0 ? static_cast<int>(std::min<int64_t>(top_k + kTopMargin, V)) : 0;
+  if (!bf16) {
+    P.slots = static_cast<int>((V + kScoreCols - 1) / kScoreCols);
+    return P;
+  }
+  P.cta_group = (o.cta_group == 1 || N <= kFewRows) ? 1 : 2;
+  P.bn = P.cta_group == 1 ? 256 : o.fwd_bn;
+  P.compact = N > kFewRows && o.fwd_compact;
+  const int64_t unit_rows = BM * P.cta_group, workers = kPlanSms / P.cta_group;
+  const int64_t mt = (N + unit_rows - 1) / unit_rows, nt = (V + P.bn - 1) / P.bn;
+  int64_t best = INT64_MAX;
+  for (int r = 1; r <= kMaxRun && r <= nt; ++r) {
+    const int64_t runs = mt * ((nt + r - 1) / r);
+    const int64_t time = (runs + workers - 1) / workers * r;
+    if (time <= best) {
+      best = time;
+      P.run = r;
+    }
+  }
+  P.slots = static_cast<int>(2 * ((nt + P.run - 1) / P.run));
+  return P;
+}
+
+// Workspace: header | row bounds (zeroed with the header) | statistics | lists |
+// row compaction.
+struct ScoreLayout {
+  size_t thr, part, lists, perm, tokens_c, block_valid, n_valid_c, hidden_c, end;
+};
+
+ScoreLayout score_layout(const ScorePlan& P, int64_t N, int64_t H) {
+  ScoreLayout L{};
+  const size_t n = static_cast<size_t>(N);
+  size_t off = kHeaderBytes;
+  L.thr = off;
+  off = align_up(off + 4 * n, 256);
+  L.part = off;
+  off = align_up(off + sizeof(float4) * n * P.slots, 256);
+  L.lists = off;
+  off = align_up(off + sizeof(TopEntry) * n * P.slots * P.K, 256);
+  if (P.compact) {
+    L.perm = off;
+    off = align_up(off + 4 * n, 256);
+    L.tokens_c = off;
+    off = align_up(off + 8 * n, 256);
+    L.block_valid = off;
+    off = align_up(off + 4 * ((n + kCompactThreads - 1) / kCompactThreads), 256);
+    L.n_valid_c = off;
+    off = align_up(off + 8, 1024);
+    L.hidden_c = off;
+    off = align_up(off + 2 * n * static_cast<size_t>(H), 256);
+  }
+  L.end = off;
+  return L;
+}
+
+// Tile indices and the partial results' row-slot product must stay in int range.
+bool score_sizes_ok(int64_t N, int64_t H, int64_t V, int32_t dtype) {
+  if (N < 0 || V < 1 || H < 8 || N > kMaxDim || V > kMaxDim || H > kMaxDim) return false;
+  if (dtype == FLCE_BF16 ? H % 8 != 0 : H > kSimtMaxH) return false;
+  if (((N + BM - 1) / BM) * ((V + BN - 1) / BN) > (int64_t{1} << 26)) return false;
+  return dtype == FLCE_BF16 || (N + 1) / 2 <= 65535;  // score_simt's grid
+}
+
+flce_status check_score(const Opts& o, const void* hidden, const void* weight, int64_t N,
+                        int64_t H, int64_t V, float softcap, double temperature, int32_t dtype,
+                        const void* ws) {
+  (void)o;
+  if (dtype != FLCE_BF16 && dtype != FLCE_FP32) return FLCE_ERR_ARG;
+  if (!(softcap >= 0.f) || !(softcap < INFINITY)) return FLCE_ERR_ARG;
+  // 1 / temperature must be a finite, normal fp32 number
+  if (!(temperature >= 1e-30) || !(temperature <= 1e30)) return FLCE_ERR_ARG;
+  if (!score_sizes_ok(N, H, V, dtype)) return FLCE_ERR_SHAPE;
+  if (N > 0 && hidden == nullptr) return FLCE_ERR_ARG;
+  if (weight == nullptr || ws == nullptr) return FLCE_ERR_ARG;
+  if (!aligned16(hidden) || !aligned16(weight)) return FLCE_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return FLCE_ERR_ARG;
+  return FLCE_OK;
+}
+
+template <class T>
+cudaError_t run_finish(const void* hidden, const void* weight, const FinishArgs& a,
+                       cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.N), 1, 1);
+  cfg.blockDim = dim3(kFinishThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t le = cudaSuccess;
+  const cudaError_t e = launch(kFwdMerge, st, [&] {
+    le = cudaLaunchKernelEx(&cfg, score_finish_kernel<T>, static_cast<const T*>(hidden),
+                            static_cast<const T*>(weight), a);
+  });
+  return le != cudaSuccess ? le : e;
+}
+
+flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout& L,
+                       const void* hidden, const void* weight, const int64_t* tokens,
+                       FinishArgs fin, float scale, char* w, cudaStream_t st) {
+  const int n = fin.N, H = fin.H;
+  const void* hid = hidden;
+  long long* n_valid_c = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (P.compact && tokens != nullptr) {
+    int* perm = reinterpret_cast<int*>(w + L.perm);
+    int64_t* tokens_c = reinterpret_cast<int64_t*>(w + L.tokens_c);
+    int* block_valid = reinterpret_cast<int*>(w + L.block_valid);
+    n_valid_c = reinterpret_cast<long long*>(w + L.n_valid_c);
+    void* hidden_c = w + L.hidden_c;
+    const int cblk = (n + kCompactThreads - 1) / kCompactThreads;
+    e = launch(kHelper, st, [&] {
+      compact_count_kernel<<<cblk, kCompactThreads, 0, st>>>(tokens, n, fin.ignore_index, fin.V,
+                                                             fin.status, block_valid);
+    });
+    if (e == cudaSuccess)
+      e = launch(kHelper, st, [&] {
+        exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(block_valid, cblk, n_valid_c);
+      });
+    if (e == cudaSuccess)
+      e = launch(kHelper, st, [&] {
+        compact_scatter_kernel<<<cblk, kCompactThreads, 0, st>>>(
+            tokens, nullptr, n, fin.ignore_index, block_valid, n_valid_c, perm, tokens_c, nullptr,
+            fin.V, nullptr, nullptr);
+      });
+    if (e == cudaSuccess)
+      e = launch(kHelper, st, [&] {
+        gather_rows_kernel<<<n, 256, 0, st>>>(static_cast<const uint4*>(hidden), H / 8, n, perm,
+                                              n_valid_c, static_cast<uint4*>(hidden_c), nullptr,
+                                              H / 4, 0);
+      });
+    if (e != cudaSuccess) return cuda_fail(e);
+    hid = hidden_c;
+    fin.perm = perm;
+    fin.n_valid = n_valid_c;
+  }
+
+  o.cta_group = P.cta_group;
+  CUtensorMap ta, tb;
+  if (!make_map(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, hid, H, n, static_cast<uint64_t>(H) * 2, BK,
+                BM) ||
+      !make_map(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, weight, H, fin.V,
+                static_cast<uint64_t>(H) * 2, BK, b_box_rows(o)))
+    return FLCE_ERR_CUDA;
+  GemmArgs g{};
+  g.k_blocks = (H + BK - 1) / BK;
+  g.group_m = o.fwd_group;
+  g.status = fin.status;
+  g.timeout_ns = o.timeout_ns;
+  g.tile_counter = o.fwd_dynamic ? ws_fwd_counter(w) : nullptr;
+  g.run_n = P.run;
+  if (n_valid_c != nullptr) {
+    g.rows_valid = n_valid_c;
+    g.rows_host = n;
+    g.rows_dim = kRowsM;
+  }
+  const GemmProblem prob{&ta, &tb, &ta, n, fin.V, g};
+  const auto score = [&](auto epi) {
+    using Epi = decltype(epi);
+    const typename Epi::Params ep{n,
+                                  fin.V,
+                                  fin.softcap,
+                                  fin.softcap > 0.f ? 1.0f / fin.softcap : 0.f,
+                                  scale,
+                                  P.run * P.bn,
+                                  P.slots,
+                                  P.K,
+                                  reinterpret_cast<float4*>(w + L.part),
+                                  reinterpret_cast<TopEntry*>(w + L.lists),
+                                  reinterpret_cast<uint32_t*>(w + L.thr)};
+    return run_gemm<Epi, false, false>(d, o, P.bn, kFwdGemm, prob, ep, nullptr, ep, st);
+  };
+  if (P.K > 0)
+    e = fin.softcap > 0.f ? score(ScoreEpi<true, true>{}) : score(ScoreEpi<false, true>{});
+  else
+    e = fin.softcap > 0.f ? score(ScoreEpi<true, false>{}) : score(ScoreEpi<false, false>{});
+  if (e == cudaSuccess) e = run_finish<__nv_bfloat16>(hidden, weight, fin, st);
+  return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
+}
+
+// Rows per block of score_simt: eight, or two where eight rows of hidden do not
+// fit shared memory (kSimtMaxH rows of two do).
+constexpr size_t kScoreSimtSmem = 200 * 1024;
+size_t score_simt_smem(int rows, int64_t H) {
+  return sizeof(float) * static_cast<size_t>(rows) * (static_cast<size_t>(H) + kScoreCols);
+}
+
+template <int kRows>
+cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishArgs& a,
+                           float scale, float4* part, TopEntry* lists, cudaStream_t st) {
+  static_assert(2 * (kSimtMaxH + kScoreCols) * sizeof(float) <= kScoreSimtSmem, "two rows fit");
+  const cudaError_t e = set_smem_attr(score_simt_kernel<kRows>, kScoreSimtSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(a.slots), static_cast<unsigned>((a.N + kRows - 1) / kRows));
+  return launch(kSimt, st, [&] {
+    score_simt_kernel<kRows><<<grid, kScoreThreads, score_simt_smem(kRows, a.H), st>>>(
+        static_cast<const float*>(hidden), static_cast<const float*>(weight), a.N, a.H, a.V,
+        a.softcap, scale, a.slots, a.K, part, lists);
+  });
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dtype,
+                                     int32_t top_k) {
+  if (dtype != FLCE_BF16 && dtype != FLCE_FP32) return 0;
+  if (!score_sizes_ok(N, H, V, dtype)) return 0;
+  if (top_k < 0 || top_k > FLCE_MAX_TOP_K || top_k > V) return 0;
+  return score_layout(score_plan(opts(), N, V, dtype == FLCE_BF16, top_k), N, H).end;
+}
+
+flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,
+                                  int64_t N, int64_t H, int64_t V, int64_t ignore_index,
+                                  float softcap, double temperature, int32_t top_k, int32_t dtype,
+                                  float* logprobs, float* entropy, float* lse,
+                                  float* top_logprobs, int64_t* top_ids, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  static_assert(FLCE_MAX_TOP_K == kMaxTopK, "header and kernels agree");
+  const Opts o = opts();
+  flce_status s = check_score(o, hidden, weight, N, H, V, softcap, temperature, dtype, workspace);
+  if (s != FLCE_OK) return s;
+  if (top_k < 0 || top_k > FLCE_MAX_TOP_K || top_k > V) return FLCE_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(tokens) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(top_ids) & 7u) != 0)
+    return FLCE_ERR_ARG;
+  if (N > 0 && (entropy == nullptr || lse == nullptr)) return FLCE_ERR_ARG;
+  if (N > 0 && (tokens == nullptr) != (logprobs == nullptr)) return FLCE_ERR_ARG;
+  if (N > 0 && top_k > 0 && (top_logprobs == nullptr || top_ids == nullptr)) return FLCE_ERR_ARG;
+  const bool bf16 = dtype == FLCE_BF16;
+  const ScorePlan P = score_plan(o, N, V, bf16, top_k);
+  const ScoreLayout L = score_layout(P, N, H);
+  if (workspace_bytes < L.end) return FLCE_ERR_WORKSPACE;
+  DevInfo* d = nullptr;
+  s = device_info(&d);
+  if (s != FLCE_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* w = static_cast<char*>(workspace);
+  // status word and tile counter, and the rows' bounds behind them
+  cudaError_t e = cudaMemsetAsync(w, 0, P.K > 0 ? L.thr + 4 * static_cast<size_t>(N) : 16, st);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (N == 0) return FLCE_OK;
+  const float scale = static_cast<float>(1.4426950408889634074 / temperature);
+  FinishArgs fin{};
+  fin.tokens = tokens;
+  fin.N = static_cast<int>(N);
+  fin.H = static_cast<int>(H);
+  fin.V = static_cast<int>(V);
+  fin.ignore_index = ignore_index;
+  fin.softcap = softcap;
+  fin.inv_temp = 1.0 / temperature;
+  fin.nat = 1.0 / (temperature * static_cast<double>(scale));
+  fin.slots = P.slots;
+  fin.K = P.K;
+  fin.top_k = top_k;
+  fin.part = reinterpret_cast<const float4*>(w + L.part);
+  fin.lists = reinterpret_cast<const TopEntry*>(w + L.lists);
+  fin.logprobs = logprobs;
+  fin.entropy = entropy;
+  fin.lse = lse;
+  fin.top_logprobs = top_logprobs;
+  fin.top_ids = top_ids;
+  fin.status = ws_status(w);
+  if (bf16) return score_bf16(d, o, P, L, hidden, weight, tokens, fin, scale, w, st);
+  float4* part = reinterpret_cast<float4*>(w + L.part);
+  TopEntry* lists = reinterpret_cast<TopEntry*>(w + L.lists);
+  e = score_simt_smem(8, H) <= kScoreSimtSmem
+          ? run_score_simt<8>(hidden, weight, fin, scale, part, lists, st)
+          : run_score_simt<2>(hidden, weight, fin, scale, part, lists, st);
+  if (e == cudaSuccess) e = run_finish<float>(hidden, weight, fin, st);
+  return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
+}
+
+flce_status flce_logprobs_backward(const void* hidden, const void* weight, const int64_t* tokens,
+                                   const float* lse, const float* entropy, int64_t N, int64_t H,
+                                   int64_t V, int64_t ignore_index, float softcap,
+                                   double temperature, int32_t dtype, const float* d_logprobs,
+                                   const float* d_entropy, float* d_hidden, float* d_weight,
+                                   int32_t flags, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  if (!(temperature >= 1e-30) || !(temperature <= 1e30)) return FLCE_ERR_ARG;
+  if (d_entropy != nullptr && N > 0 && entropy == nullptr) return FLCE_ERR_ARG;
+  const RowGrads rg{d_logprobs, d_entropy, entropy, static_cast<float>(1.0 / temperature)};
+  return backward_any(hidden, weight, tokens, lse, N, H, V, ignore_index, softcap, FLCE_SUM, dtype,
+                      nullptr, 1.0f, -1, nullptr, d_hidden, d_weight, flags, workspace,
+                      workspace_bytes, stream, &rg);
+}
+
+}  // extern "C"

@@ -255,6 +255,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// max that keeps a NaN of either argument
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ---------------------------------------------------------------- dependent launch
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialisation may start before the previous kernel on its stream has

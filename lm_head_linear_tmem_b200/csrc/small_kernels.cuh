@@ -688,14 +688,47 @@ __device__ __forceinline__ float simt_grad_scale(const float* grad_output, float
   return g;
 }
 
+// Upstream gradients of the scoring operator (see DzEpi's kRowGrads): either
+// may be null (zero).
+struct RowGrads {
+  const float* d_logprobs;  // [N]
+  const float* d_entropy;   // [N]
+  const float* entropy;     // [N]
+  float inv_temp;
+};
+
+// dZ of one logit z of a row in the loss; `hit`: the row's label.
+// kRowGrads: the scoring operator's gradient, else the loss's.
+template <bool kRowGrads>
+__device__ __forceinline__ float simt_dz(float z, bool hit, float lse, float softcap, float g,
+                                         const RowGrads& rg, int row) {
+  const float L = capped(z, softcap);
+  float d;
+  if constexpr (kRowGrads) {
+    const float logp = max_nan(fmaf(L, rg.inv_temp, -lse), kLowExp2 * kLn2);
+    const float a = rg.d_logprobs != nullptr ? rg.d_logprobs[row] : 0.f;
+    const float b = rg.d_entropy != nullptr ? rg.d_entropy[row] : 0.f;
+    const float e = rg.d_entropy != nullptr ? rg.entropy[row] : 0.f;
+    d = ((hit ? a : 0.f) - expf(logp) * fmaf(b, logp + e, a)) * rg.inv_temp;
+  } else {
+    d = expf(L - lse) - (hit ? 1.f : 0.f);
+  }
+  if (softcap > 0.f) {
+    const float u = L / softcap;
+    d *= 1.f - u * u;
+  }
+  return g * d;
+}
+
 // One block per token row: dHidden[row] = sum_v dZ[row, v] W[v].
 // Dynamic smem: 2*H + kSimtChunk floats.
+template <bool kRowGrads>
 __global__ void __launch_bounds__(kSimtThreads)
     simt_dh_kernel(const float* __restrict__ hidden, const float* __restrict__ weight,
                    const int64_t* __restrict__ labels, const float* __restrict__ lse, int N,
                    int H, int V, int64_t ignore_index, float softcap, const float* grad_output,
                    float grad_scale, const long long* n_valid, int mean, int accumulate,
-                   float* __restrict__ d_hidden) {
+                   float* __restrict__ d_hidden, const RowGrads rg) {
   extern __shared__ float sh[];
   float* h = sh;
   float* acc = sh + H;
@@ -720,13 +753,7 @@ __global__ void __launch_bounds__(kSimtThreads)
         const float* w = weight + static_cast<size_t>(v) * H;
         float z = 0.f;
         for (int k = 0; k < H; ++k) z = fmaf(h[k], w[k], z);
-        const float L = capped(z, softcap);
-        float d = expf(L - l) - (v == y ? 1.f : 0.f);
-        if (softcap > 0.f) {
-          const float u = L / softcap;
-          d *= 1.f - u * u;
-        }
-        gz = g * d;
+        gz = simt_dz<kRowGrads>(z, v == y, l, softcap, g, rg, row);
       }
       G[j] = gz;
     }
@@ -746,12 +773,13 @@ __global__ void __launch_bounds__(kSimtThreads)
 
 // One block per vocab row: dWeight[v] = sum_i dZ[i, v] hidden[i].
 // Dynamic smem: 2*H + kSimtThreads floats.
+template <bool kRowGrads>
 __global__ void __launch_bounds__(kSimtThreads)
     simt_dw_kernel(const float* __restrict__ hidden, const float* __restrict__ weight,
                    const int64_t* __restrict__ labels, const float* __restrict__ lse, int N,
                    int H, int V, int64_t ignore_index, float softcap, const float* grad_output,
                    float grad_scale, const long long* n_valid, int mean, int accumulate,
-                   float* __restrict__ d_weight) {
+                   float* __restrict__ d_weight, const RowGrads rg) {
   extern __shared__ float sh[];
   float* w = sh;
   float* acc = sh + H;
@@ -774,13 +802,7 @@ __global__ void __launch_bounds__(kSimtThreads)
         const float* hi = hidden + static_cast<size_t>(i) * H;
         float z = 0.f;
         for (int k = 0; k < H; ++k) z = fmaf(hi[k], w[k], z);
-        const float L = capped(z, softcap);
-        float d = expf(L - lse[i]) - (v == y ? 1.f : 0.f);
-        if (softcap > 0.f) {
-          const float u = L / softcap;
-          d *= 1.f - u * u;
-        }
-        gz = g * d;
+        gz = simt_dz<kRowGrads>(z, v == y, lse[i], softcap, g, rg, i);
       }
       G[t] = gz;
     }

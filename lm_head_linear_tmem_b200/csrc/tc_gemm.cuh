@@ -94,6 +94,9 @@ constexpr uint32_t kStatusLabelRange = 1u;
 constexpr uint32_t kStatusTimeout = 2u;
 
 constexpr float kLog2e = 1.4426950408889634f;
+// exp2 of anything below is 0 in fp32; as a lower bound of a log2 probability it
+// keeps (-inf) * 0 out of the sums of p log p.
+constexpr float kLowExp2 = -200.0f;
 
 // tanh from one SFU exp2 and one fast division, by the identity
 // tanh(x) = sign(x) * (1 - e^{-2|x|}) / (1 + e^{-2|x|}).  e^{-2|x|} lies in
@@ -144,6 +147,9 @@ struct GemmArgs {
   // rows) instead of the 2-D view (one 8 KiB box per chunk).  Fewer, larger
   // TMA requests: 76.7 vs 68.9 B/clk per SM measured into shared memory.
   int a_mn3d, b_mn3d;
+  // Epilogues that carry a row's state from tile to tile (Epi::kRun): tiles are
+  // handed out in runs of up to run_n consecutive column tiles of one row tile.
+  int run_n;
 };
 
 constexpr int kRowsNone = 0;
@@ -163,6 +169,20 @@ __device__ __forceinline__ void tile_coords(int tile, const GemmArgs& g, int& mb
   const int r = tile - grp * per_group;
   mb = first_m + r % gm;
   nb = r / gm;
+}
+
+// The same for runs of run_n column tiles (tile index = run * run_n + position
+// in the run): runs are walked in the raster order of tile_coords.
+__device__ __forceinline__ void run_tile_coords(int tile, const GemmArgs& g, int& mb, int& nb) {
+  const int run = tile / g.run_n;
+  const int runs_n = (g.n_tiles + g.run_n - 1) / g.run_n;
+  const int per_group = g.group_m * runs_n;
+  const int grp = run / per_group;
+  const int first_m = grp * g.group_m;
+  const int gm = min(g.group_m, g.m_tiles - first_m);
+  const int r = run - grp * per_group;
+  mb = first_m + r % gm;
+  nb = (r / gm) * g.run_n + (tile - run * g.run_n);
 }
 
 // Hand the accumulator back to the MMA issuer: `tempty_bar` is the
@@ -209,6 +229,8 @@ __device__ __forceinline__ void stage_row_128b(uint8_t* buf, int lane, const uin
 // mbarrier; bounded waits), which merges and writes them.
 template <bool kSoftcap>
 struct FwdStatsEpi {
+  using State = int;  // banks seen by this warp
+  static constexpr bool kRun = false;
   static constexpr int kEpiWarps = 8;
   // first warp of a quadrant: its mbarriers full[2], empty[2]; second warp:
   // the two (m[32], s[32]) slots
@@ -395,8 +417,17 @@ struct FwdStatsEpi {
 // With `resid` set, the label entry's rounding residual d - bf16(d) (exact in
 // fp32) is recorded per row, for the fp32 corrections that make the label
 // term of dHidden and dWeight exact.
-template <bool kSoftcap>
+//
+// kRowGrads: the gradient of the scoring operator instead, whose upstream
+// gradients are two numbers per row, a of its log probability and b of its
+// entropy E (x = L / temperature, log p = x - lse):
+//   dZ = ([v == y] * a - p * (a + b * (log p + E))) / temperature * softcap'
+// They differ from row to row, so they go into the bf16 value; the label entry's
+// residual is taken as above.
+template <bool kSoftcap, bool kRowGrads = false>
 struct DzEpi {
+  using State = int;  // TMA stores issued by this warp
+  static constexpr bool kRun = false;
   // Eight warps: the two warps of a TMEM lane quadrant each take 128 of a
   // bank's columns.  One 4 KiB staging buffer per warp (32 rows x 64 bf16).
   static constexpr int kEpiWarps = 8;
@@ -414,17 +445,36 @@ struct DzEpi {
     float inv_softcap;
     float* resid;      // [token rows] or null
     int64_t v_total;   // V: a label outside [0, V) counts as ignored
+    // kRowGrads: upstream gradients and entropies in token order (either
+    // gradient may be null: zero), perm[row] the token row of a row (null: same)
+    const float* d_logprobs;
+    const float* d_entropy;
+    const float* entropy;
+    const int* perm;
+    float inv_temp;
   };
 
   // The row's label and lse, read before the accumulator is ready.
+  // With kRowGrads also a / temperature, b / temperature and (a + b E) / temperature.
   struct Pre {
     int64_t y;
     float lse;
+    float a, b, c;
   };
   __device__ static Pre prepare(const Params& p, int m_base, int q, int lane) {
     const int row_l = m_base + q * 32 + lane;
-    if (row_l >= p.rows) return Pre{0, 0.f};
-    return Pre{p.labels[p.t0 + row_l], p.lse[p.t0 + row_l]};
+    if (row_l >= p.rows) return Pre{0, 0.f, 0.f, 0.f, 0.f};
+    Pre pre{p.labels[p.t0 + row_l], p.lse[p.t0 + row_l], 0.f, 0.f, 0.f};
+    if constexpr (kRowGrads) {
+      const int row = p.perm != nullptr ? p.perm[p.t0 + row_l] : p.t0 + row_l;
+      if (p.d_logprobs != nullptr) pre.a = p.d_logprobs[row] * p.inv_temp;
+      pre.c = pre.a;
+      if (p.d_entropy != nullptr) {
+        pre.b = p.d_entropy[row] * p.inv_temp;
+        pre.c = fmaf(pre.b, p.entropy[row], pre.a);
+      }
+    }
+    return pre;
   }
 
   __device__ static bool tile(const Params& p, const Pre& pre, int m_base, int col0,
@@ -459,7 +509,23 @@ struct DzEpi {
     // 16 bf16 pairs into r[0..15] (in place: no second register array)
     auto dz32 = [&](int c0l, uint32_t(&r)[32]) {
       // d overwrites the logit it comes from
-      if constexpr (kSoftcap) {
+      if constexpr (kRowGrads) {
+        const float scale = p.inv_temp * kLog2e;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float L = __uint_as_float(r[j]), f = 1.0f;
+          if constexpr (kSoftcap) {
+            L = p.softcap * tanh_exp2(L * p.inv_softcap);
+            const float u = L * p.inv_softcap;
+            f = fmaf(-u, u, 1.0f);
+          }
+          const float lp2 = max_nan(fmaf(L, scale, -lse2), kLowExp2);  // log2 p
+          const float pr = ex2_approx(lp2);
+          const float qv = fmaf(pre.b * kLn2, lp2, pre.c);
+          r[j] = __float_as_uint(
+              f * (any_label && c0l + j == y_local ? fmaf(-pr, qv, pre.a) : -pr * qv));
+        }
+      } else if constexpr (kSoftcap) {
         float f[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -570,6 +636,8 @@ struct DzEpi {
 // when `reduce` (accumulation across chunks of the split reduction dimension).
 // g = grad_output * grad_scale, divided by max(n, 1) for 'mean'.
 struct StoreEpi {
+  using State = int;  // TMA stores issued by this warp
+  static constexpr bool kRun = false;
   // Eight warps: the two warps of a TMEM lane quadrant each take 128 of a
   // bank's columns.  One 4 KiB staging buffer per warp (32 rows x 32 fp32).
   static constexpr int kEpiWarps = 8;
@@ -787,14 +855,22 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
   };
   const GemmArgs a0 = bound_rows(g0);
   const GemmArgs a1 = bound_rows(g1);
-  const int tiles0 = a0.m_tiles * a0.n_tiles;
-  const int num_tiles = tiles0 + a1.m_tiles * a1.n_tiles;
+  // (runs: one problem, every run counted as run_n tile indices)
+  const int tiles0 = Epi::kRun
+      ? a0.m_tiles * ((a0.n_tiles + a0.run_n - 1) / a0.run_n) * a0.run_n
+      : a0.m_tiles * a0.n_tiles;
+  const int num_tiles = Epi::kRun ? tiles0 : tiles0 + a1.m_tiles * a1.n_tiles;
   const int unit = blockIdx.x / kCG;  // CTA (kCG = 1) or CTA pair (kCG = 2)
   const int n_units = gridDim.x / kCG;
   volatile int* abort_flag = &abort_sh;
 
   // problem, its args and the tile's coordinates for global tile index t
   auto locate = [&](int t, int& prob, int& mb, int& nb) {
+    if constexpr (Epi::kRun) {
+      prob = 0;
+      run_tile_coords(t, a0, mb, nb);
+      return;
+    }
     prob = (t < tiles0) ? 0 : 1;
     tile_coords(prob ? t - tiles0 : t, prob ? a1 : a0, mb, nb);
   };
@@ -847,11 +923,33 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
       bool ok = true;
       int rslot = 0;
       uint32_t rph = 0;
+      int run_next = 0, run_end = 0;  // Epi::kRun: tiles left of the run in hand
       for (int k = 0; ok; ++k) {
         int tile;
         if (leader) {
-          tile = (g0.tile_counter != nullptr) ? atomicAdd(g0.tile_counter, 1) : unit + k * n_units;
-          if (tile > num_tiles) tile = num_tiles;
+          if constexpr (Epi::kRun) {
+            if (run_next == run_end) {  // take the next run: k counts runs here
+              const int run = (g0.tile_counter != nullptr) ? atomicAdd(g0.tile_counter, 1)
+                                                           : unit + k * n_units;
+              // (run < num_tiles first: the product must not wrap past the last run)
+              if (run < num_tiles && run * a0.run_n < num_tiles) {
+                int mb, nb;
+                run_tile_coords(run * a0.run_n, a0, mb, nb);
+                run_next = run * a0.run_n;
+                run_end = run_next + min(a0.run_n, a0.n_tiles - nb);
+              } else {
+                run_next = num_tiles;
+                run_end = num_tiles + 1;
+              }
+            } else {
+              --k;
+            }
+            tile = run_next++;
+          } else {
+            tile = (g0.tile_counter != nullptr) ? atomicAdd(g0.tile_counter, 1)
+                                                : unit + k * n_units;
+            if (tile > num_tiles) tile = num_tiles;
+          }
           ok = ring_publish(rslot, rph, tile);
         } else {
           ok = ring_take(rslot, rph, false, tile);
@@ -1070,7 +1168,7 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
     const int part = (warp - 2) >> 2;   // which half of a bank
     uint8_t* stg = smem + kStages * Cfg::kStageBytes + (warp - 2) * Epi::kStagingPerWarp;
     int it = 0;
-    int nstore = 0;  // TMA stores issued by this warp (selects the staging buffer)
+    typename Epi::State state{};
     bool ok = true;
     if (g0.wait_counter != nullptr) {
       // the launch that last read what this one overwrites has finished
@@ -1121,7 +1219,7 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
         const uint32_t tempty_local = smem_u32(&bar_tempty[bank]);
         const uint32_t tempty = (kCG == 1) ? tempty_local : mapa_shared(tempty_local, 0);
         if (!Epi::tile(prob ? ep1 : ep0, pre, m_base, nb * kBN + h * BN, taddr, q, lane, part,
-                       stg, prob ? &tmOut1 : &tmOut0, tempty, nstore, ga.k_blocks == 0,
+                       stg, prob ? &tmOut1 : &tmOut0, tempty, state, ga.k_blocks == 0,
                        abort_flag, g0.timeout_ns)) {
           ok = false;
           break;

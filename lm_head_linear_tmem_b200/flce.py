@@ -22,6 +22,7 @@ API (names follow the pages):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple, Optional, Tuple
 
@@ -51,10 +52,19 @@ def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _prep(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor):
-    if not (hidden.is_cuda and weight.is_cuda and labels.is_cuda):
+def on_device(device: torch.device):
+    """The library works on the current device: make it the tensors' (nothing to do,
+    and nothing paid, where it is)."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _prep(hidden: torch.Tensor, weight: torch.Tensor, labels: Optional[torch.Tensor]):
+    given = [t for t in (hidden, weight, labels) if t is not None]
+    if not all(t.is_cuda for t in given):
         raise ValueError("hidden, weight and labels must be CUDA tensors")
-    if hidden.device != weight.device or hidden.device != labels.device:
+    if any(t.device != hidden.device for t in given):
         raise ValueError("hidden, weight and labels must be on one device")
     if hidden.dtype not in _DTYPES or weight.dtype != hidden.dtype:
         raise TypeError("hidden and weight must both be bfloat16 or both float32")
@@ -64,6 +74,8 @@ def _prep(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor):
     if hidden.shape[-1] != H:
         raise ValueError("hidden's last dim must equal weight.shape[1]")
     h2 = hidden.reshape(-1, H).contiguous()
+    if labels is None:
+        return h2, weight.contiguous(), None
     y = labels.reshape(-1)
     if y.dtype != torch.int64:
         y = y.to(torch.int64)
@@ -86,6 +98,12 @@ def alloc_workspace(N: int, H: int, V: int, dtype: torch.dtype, device,
     if n == 0:
         raise ValueError("invalid FLCE sizes or flags")
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def check_workspace(workspace: torch.Tensor, device: torch.device) -> None:
+    if workspace.device != device or workspace.dtype != torch.uint8 \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
 
 
 def status(workspace: torch.Tensor) -> int:
@@ -133,29 +151,12 @@ def forward(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
     return FlceForward(loss, ntok, lse)
 
 
-def backward(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
-             lse: torch.Tensor, grad_output: Optional[torch.Tensor] = None,
-             grad_scale: float = 1.0, num_valid: Optional[torch.Tensor] = None,
-             num_label_tokens: Optional[int] = None,
-             ignore_index: int = -100, softcap: float = 0.0, reduction: str = "sum",
-             workspace: Optional[torch.Tensor] = None,
-             d_hidden: Optional[torch.Tensor] = None, d_weight: Optional[torch.Tensor] = None,
-             accumulate_d_hidden: bool = False, accumulate_d_weight: bool = False,
-             grad_dtype: torch.dtype = torch.float32,
-             compute_d_hidden: bool = True, compute_d_weight: bool = True,
-             check_status: bool = False) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
-    """dHidden [N, H] and dWeight [V, H], float32 or bfloat16 (the dtype of a
-    given d_hidden / d_weight, else `grad_dtype`).  A bf16 gradient is
-    computed in fp32 and rounded once.  With accumulate_* the gradient is
-    added into the given d_hidden / d_weight instead of overwriting them (e.g.
-    over the micro-batches of one optimizer step).  compute_d_weight=False
-    (a frozen LM head) or compute_d_hidden=False skips that gradient's GEMM
-    and returns None in its place.  num_label_tokens as for forward: the
-    gradient of the normalised 'sum' loss."""
-    h2, w, y = _prep(hidden, weight, labels)
-    N, H = h2.shape
-    V = w.shape[0]
-    dev = h2.device
+def alloc_grads(N: int, H: int, V: int, dev, d_hidden: Optional[torch.Tensor],
+                d_weight: Optional[torch.Tensor], accumulate_d_hidden: bool,
+                accumulate_d_weight: bool, grad_dtype: torch.dtype, compute_d_hidden: bool,
+                compute_d_weight: bool):
+    """The gradient buffers of a backward call (given ones checked, others made, None for one
+    that is not computed) and the library's flags for them."""
     if grad_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("grad_dtype must be float32 or bfloat16")
     if not (compute_d_hidden or compute_d_weight):
@@ -186,6 +187,35 @@ def backward(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
                 and d_hidden.dtype == torch.bfloat16 else 0)
              | (_native.DWEIGHT_BF16 if d_weight is not None
                 and d_weight.dtype == torch.bfloat16 else 0))
+    return d_hidden, d_weight, flags
+
+
+def backward(hidden: torch.Tensor, weight: torch.Tensor, labels: torch.Tensor,
+             lse: torch.Tensor, grad_output: Optional[torch.Tensor] = None,
+             grad_scale: float = 1.0, num_valid: Optional[torch.Tensor] = None,
+             num_label_tokens: Optional[int] = None,
+             ignore_index: int = -100, softcap: float = 0.0, reduction: str = "sum",
+             workspace: Optional[torch.Tensor] = None,
+             d_hidden: Optional[torch.Tensor] = None, d_weight: Optional[torch.Tensor] = None,
+             accumulate_d_hidden: bool = False, accumulate_d_weight: bool = False,
+             grad_dtype: torch.dtype = torch.float32,
+             compute_d_hidden: bool = True, compute_d_weight: bool = True,
+             check_status: bool = False) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """dHidden [N, H] and dWeight [V, H], float32 or bfloat16 (the dtype of a
+    given d_hidden / d_weight, else `grad_dtype`).  A bf16 gradient is
+    computed in fp32 and rounded once.  With accumulate_* the gradient is
+    added into the given d_hidden / d_weight instead of overwriting them (e.g.
+    over the micro-batches of one optimizer step).  compute_d_weight=False
+    (a frozen LM head) or compute_d_hidden=False skips that gradient's GEMM
+    and returns None in its place.  num_label_tokens as for forward: the
+    gradient of the normalised 'sum' loss."""
+    h2, w, y = _prep(hidden, weight, labels)
+    N, H = h2.shape
+    V = w.shape[0]
+    dev = h2.device
+    d_hidden, d_weight, flags = alloc_grads(N, H, V, dev, d_hidden, d_weight, accumulate_d_hidden,
+                                            accumulate_d_weight, grad_dtype, compute_d_hidden,
+                                            compute_d_weight)
     if workspace is None:
         workspace = alloc_workspace(N, H, V, h2.dtype, dev, flags)
     if grad_output is not None:
