@@ -253,15 +253,17 @@ flce_status flce_backward_ex(const void* hidden, const void* weight, const int64
  * like flce_forward without writing the [N, V] logits.  The logits of the listed
  * ids and of the given token are evaluated in float64 from the inputs, and the
  * alternatives are ordered by those (before softcap and temperature, which keep
- * the order); they are picked by float32 logits, of which top_k + 4 are kept.
+ * the order); they are picked by float32 logits, of which at least top_k + 4 are
+ * kept.  lse and entropy take the terms of the kept logits from float64 too.
  *
  * A row whose token is ignore_index takes no part: logprobs, entropy, lse and
  * top_logprobs 0, top_ids -1.  A token outside [0, V) is reported as
  * FLCE_ERR_LABEL_RANGE and its row treated the same way.  Logits of -inf are
  * probabilities of 0 (they add nothing to the entropy and are never
  * alternatives); where fewer than top_k logits lie above -inf the places left
- * hold id -1 and log probability -inf.  A NaN or +inf logit makes lse, entropy and log
- * probabilities of its row NaN. */
+ * hold id -1 and log probability -inf.  A NaN or +inf logit makes
+ * lse, entropy and log probabilities of its row NaN (which ids a row with a NaN
+ * logit lists is not defined). */
 
 /* Largest top_k. */
 #define FLCE_MAX_TOP_K 32
@@ -277,7 +279,9 @@ size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dt
  *   temperature   host double in [1e-30, 1e30]
  *   top_k         0 .. min(V, FLCE_MAX_TOP_K); 0: no alternatives, the last two outputs unused
  *   logprobs      device float[N]
- *   entropy, lse  device float[N]        (flce_logprobs_backward reads both)
+ *   entropy, lse  device float[N]
+ *   saved         device float[2 * N]    what flce_logprobs_backward reads: lse and entropy
+ *                                        of the logits as the matrix product rounds them
  *   top_logprobs  device float[N * top_k]
  *   top_ids       device int64[N * top_k]
  * Every other argument as flce_forward.  FLCE_FP32 runs on CUDA cores and takes
@@ -285,7 +289,7 @@ size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dt
 flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,
                                   int64_t N, int64_t H, int64_t V, int64_t ignore_index,
                                   float softcap, double temperature, int32_t top_k, int32_t dtype,
-                                  float* logprobs, float* entropy, float* lse,
+                                  float* logprobs, float* entropy, float* lse, float* saved,
                                   float* top_logprobs, int64_t* top_ids, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
@@ -294,16 +298,15 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
  *   dZ_iv = ([v == y_i] a_i - p_iv (a_i + b_i (log p_iv + entropy_i))) / T
  *           * (softcap > 0 ? 1 - (L_iv/softcap)^2 : 1),  0 on rows that take no part
  *   d_hidden = dZ . weight,  d_weight = dZ^T . hidden
- * lse and entropy are the forward's outputs.  d_hidden, d_weight, flags and the
+ * with p and entropy from the forward's `saved`.  d_hidden, d_weight, flags and the
  * workspace (flce_workspace_bytes_ex) as flce_backward.  Gradients do not flow
  * through top_logprobs. */
 flce_status flce_logprobs_backward(const void* hidden, const void* weight, const int64_t* tokens,
-                                   const float* lse, const float* entropy, int64_t N, int64_t H,
-                                   int64_t V, int64_t ignore_index, float softcap,
-                                   double temperature, int32_t dtype, const float* d_logprobs,
-                                   const float* d_entropy, float* d_hidden, float* d_weight,
-                                   int32_t flags, void* workspace, size_t workspace_bytes,
-                                   void* stream);
+                                   const float* saved, int64_t N, int64_t H, int64_t V,
+                                   int64_t ignore_index, float softcap, double temperature,
+                                   int32_t dtype, const float* d_logprobs, const float* d_entropy,
+                                   float* d_hidden, float* d_weight, int32_t flags,
+                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Size of the library-owned device buffer behind flce_forward_noalloc. */
 #define FLCE_NOALLOC_SCRATCH_BYTES (16u * 1024u * 1024u)

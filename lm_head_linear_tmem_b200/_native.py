@@ -56,11 +56,11 @@ SIGNATURES = {
                                  c_size, c_vp]),
     "flce_logprobs_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i32, c_i32]),
     "flce_logprobs_forward": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32, c_f64,
-                                      c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_size,
-                                      c_vp]),
-    "flce_logprobs_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64,
-                                       c_f32, c_f64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
-                                       c_size, c_vp]),
+                                      c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                      c_size, c_vp]),
+    "flce_logprobs_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,
+                                       c_f64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_size,
+                                       c_vp]),
     "flce_set_option": (c_i32, [c_i32, c_i64]),
     "flce_get_option": (c_i32, [c_i32, ctypes.POINTER(c_i64)]),
     "flce_forward_noalloc": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,

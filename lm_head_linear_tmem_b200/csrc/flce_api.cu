@@ -482,10 +482,10 @@ template <class Epi, int kCG, int kBN, bool kAMn0, bool kBMn0, bool kAMn1, bool 
 cudaError_t run_gemm_cg(DevInfo* d, int kind, const GemmProblem& p0,
                         const typename Epi::Params& ep0, const GemmProblem* p1,
                         const typename Epi::Params& ep1, cudaStream_t st, int* ctas_out) {
-  using Cfg = TileCfg<kCG, kBN>;
+  using Cfg = EpiTileCfg<Epi, kCG, kBN>;
   auto k = tc_gemm_kernel<Epi, kCG, kBN, kAMn0, kBMn0, kAMn1, kBMn1>;
   constexpr size_t kSmem = gemm_smem_bytes<Epi, kCG, kBN>();
-  static_assert(kSmem <= 227 * 1024 - 512, "shared memory");
+  static_assert(kSmem <= kMaxGemmSmem, "shared memory");
   cudaError_t e = set_smem_attr(k, kSmem);
   if (e != cudaSuccess) return e;
   GemmArgs g0 = p0.g;
@@ -499,8 +499,8 @@ cudaError_t run_gemm_cg(DevInfo* d, int kind, const GemmProblem& p0,
     g1.m_tiles = g1.n_tiles = 0;
   }
   const GemmProblem& q1 = p1 ? *p1 : p0;
-  // what is handed out: tiles, or runs of run_n column tiles
-  const int tiles = Epi::kRun ? g0.m_tiles * ((g0.n_tiles + g0.run_n - 1) / g0.run_n)
+  // what is handed out: tiles, or runs of column tiles
+  const int tiles = Epi::kRun ? g0.m_tiles * g0.runs
                               : g0.m_tiles * g0.n_tiles + g1.m_tiles * g1.n_tiles;
   const int units = std::max(1, std::min(tiles, d->sms / kCG));
   if (ctas_out != nullptr) *ctas_out = units * kCG;

@@ -18,8 +18,10 @@ namespace flce {
 // kTopMargin more, because the lists are ordered by the tensor cores' fp32 logits
 // and the final order by the logits in fp64: an alternative is lost only if more
 // than kTopMargin others stand between its fp32 rank and top_k.
+// Every row keeps at least kMinTopList: see the correction in score_finish.
 constexpr int kMaxTopK = 32;
 constexpr int kTopMargin = 4;
+constexpr int kMinTopList = 8;
 constexpr int kMaxTopList = kMaxTopK + kTopMargin;
 
 // A running maximum that nothing has been merged into.  Finite, so that the
@@ -34,6 +36,11 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __device__ __forceinline__ float order_value(uint32_t k) {
   if (k == 0u) return -CUDART_INF_F;
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// The largest float below v (not NaN); -inf stays.
+__device__ __forceinline__ float nextbelow(float v) {
+  return v == -CUDART_INF_F ? v : v == 0.f ? -1.4e-45f : order_value(order_key(v) - 1u);
 }
 
 // Statistics of a set of values x (in the log2 domain): m their maximum,
@@ -60,28 +67,39 @@ __device__ __forceinline__ void stats_merge(Stats& a, Stats b) {
 }
 
 // One entry of a list of large logits: the logit before softcap and temperature
-// (both keep the order) and its vocabulary id; id -1: no entry.
+// (both keep the order; > -inf) and its vocabulary id.
 struct TopEntry {
   float v;
   int id;
 };
+// The order of alternatives (entries with different ids).
+__device__ __forceinline__ bool better(TopEntry a, TopEntry b) {
+  return a.v > b.v || (a.v == b.v && a.id < b.id);
+}
 
 // ------------------------------------------------------------------ GEMM epilogue
 // A CTA works on runs of consecutive column tiles of one row tile, so a thread
 // sees one row's logits over a long range of columns and keeps that row's state
-// in registers (statistics) and local memory (list) until the run ends:
+// in registers (statistics) and shared memory (list) until the run ends:
 // partial results per row and run instead of per row and tile, and a list that
 // soon turns nearly every column down with one comparison of the maximum of 32.
-// `thr` holds, per row, the largest known K-th best logit of any run (a lower
-// bound of the row's K-th best): later runs start from it.  A logit below it
-// cannot be among the K best; equal ones are kept, because a lower id wins.
-// The K best by (logit, lowest id) are in the lists whatever the order in
-// which runs are worked on, so the results do not depend on it.
-template <bool kSoftcap, bool kTop>
+// `seen` holds, for each row, the maxima of K groups of the columns that any CTA
+// has seen (32-column chunks, dealt out in turn): the least of them is a lower
+// bound of the row's K-th best.  With it the lists of later runs start where the
+// earlier ones have got to: about ln(K + 1) K / n of the columns are candidates
+// after n columns.  A logit below the bound cannot be among the K best; equal ones
+// are kept, because a lower id wins.  The K best by (logit, lowest id) are in the
+// lists whatever the order in which runs are worked on, so the results do not
+// depend on it.
+// kCap: entries a list has room for.  16 fit beside the four-stage operand ring
+// of the other epilogues; kMaxTopList leave three stages.
+constexpr int kSmallTopList = 16;
+
+template <bool kSoftcap, int kCap>
 struct ScoreEpi {
   static constexpr bool kRun = true;
   static constexpr int kEpiWarps = 8;
-  static constexpr int kStagingPerWarp = 0;
+  static constexpr int kStagingPerWarp = 32 * kCap * 8;  // [kCap][32] values, then ids
   __device__ static void init_smem(uint8_t*) {}
 
   struct Params {
@@ -90,63 +108,137 @@ struct ScoreEpi {
     float softcap;
     float inv_softcap;
     float scale;      // log2(e) / temperature
-    int run_cols;     // columns of a full run
+    RunMap map;
+    int tile_cols;
     int slots;        // 2 * runs per row (the two warps of a row, half a bank each)
-    int K;            // list length
-    float4* part;     // [N][slots]: m, s, t
-    TopEntry* lists;  // [N][slots][K], best first
-    uint32_t* thr;    // [N] order_key of the bound; zeroed before the launch
+    int K;            // list length, at most kCap
+    float4* part;     // [N][slots]: m, s, t, largest entry of the list (-inf: none)
+    int* count;       // [N][slots]: entries of the list
+    TopEntry* lists;  // [N][slots][K], in no order
+    uint32_t* seen;   // [K][N] order_key of the groups' maxima; zeroed before the launch
   };
 
+  // The list is not sorted: a candidate takes the place of the worst entry (-inf
+  // while there is room), and one pass over the values, whose loads do not wait
+  // for one another, finds the next worst.  All lanes go through that together:
+  // left to diverge, the lanes' passes ran one after another, 13000 clocks for
+  // 32 columns.
   struct State {
     Stats st;
-    float kth;        // the list's last value: -inf until it is full
-    float told;       // largest bound written to or read from thr
-    float lv[kTop ? kMaxTopList : 1];
-    int li[kTop ? kMaxTopList : 1];
+    float kth;    // value of the worst entry
+    int worst;    // place of the worst entry
   };
 
   struct Pre {
-    float thr;
+    float bound;
   };
   __device__ static Pre prepare(const Params& p, int m_base, int q, int lane) {
-    if constexpr (!kTop) return Pre{0.f};
     const int row = m_base + q * 32 + lane;
     if (row >= p.N) return Pre{CUDART_INF_F};
-    return Pre{order_value(*reinterpret_cast<const volatile uint32_t*>(p.thr + row))};
+    uint32_t least = 0xffffffffu;
+    const volatile uint32_t* g = p.seen + row;
+#pragma unroll 4
+    for (int i = 0; i < p.K; ++i) least = min(least, g[static_cast<size_t>(i) * p.N]);
+    return Pre{order_value(least)};
   }
 
-  // Keeps the list sorted by (value descending, id ascending); ids arrive in
-  // ascending order, so an equal value goes behind those already there.
-  __device__ static void insert(State& S, int K, float v, int id) {
-    int i = K - 1;
-    for (; i > 0 && S.lv[i - 1] < v; --i) {
-      S.lv[i] = S.lv[i - 1];
-      S.li[i] = S.li[i - 1];
+  // This lane's list: entry i at lv[32 * i], li[32 * i].
+  struct List {
+    float* lv;
+    int* li;
+  };
+
+  // The lanes with `take` (v > S.kth) put an entry into their lists.  Ids come in
+  // ascending order, so of equal values the one with the highest id is the worst
+  // and a newcomer equal to the worst stays out.
+  __device__ static void put(State& S, List L, int K, bool take, float v, int id) {
+    if (take) {
+      L.lv[32 * S.worst] = v;
+      L.li[32 * S.worst] = id;
     }
-    S.lv[i] = v;
-    S.li[i] = id;
-    S.kth = S.lv[K - 1];
+    __syncwarp();
+    float mv = CUDART_INF_F;
+    int at = 0;
+    bool equal = false;
+#pragma unroll 4
+    for (int i = 0; i < K; ++i) {
+      const float x = L.lv[32 * i];
+      equal = x == mv || (equal && x >= mv);
+      at = x < mv ? i : at;
+      mv = fminf(mv, x);
+    }
+    equal = take && equal && mv > -CUDART_INF_F;
+    if (__any_sync(0xffffffffu, equal)) {
+      for (int i = 0; i < K; ++i)
+        if (L.lv[32 * i] == mv && L.li[32 * i] > L.li[32 * at]) at = equal ? i : at;
+      __syncwarp();
+    }
+    S.kth = take ? mv : S.kth;
+    S.worst = take ? at : S.worst;
   }
 
-  // The candidates among 32 columns starting at `col`, `mx` their maximum.
-  __device__ static void scan32(State& S, const Params& p, float thr, const uint32_t (&r)[32],
-                                float mx, int col) {
-    if (!__any_sync(0xffffffffu, mx > S.kth && mx >= thr)) return;
-    float qv[32];
-    int qc[32];
-    int n = 0;
+  // r[j] of a lane's own j, by halving: local memory (what an indexed array would
+  // become) has no room in the L1 beside the operand ring and took 3000 clocks a
+  // chunk and more.
+  __device__ static float pick(const uint32_t (&r)[32], int j) {
+    uint32_t x[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float v = __uint_as_float(r[j]);
-      if (v > S.kth && v >= thr) {
-        qv[n] = v;
-        qc[n] = col + j;
-        ++n;
-      }
+    for (int i = 0; i < 16; ++i) x[i] = (j & 16) ? r[i + 16] : r[i];
+#pragma unroll
+    for (int w = 8; w >= 1; w /= 2)
+#pragma unroll
+      for (int i = 0; i < w; ++i) x[i] = (j & w) ? x[i + w] : x[i];
+    return __uint_as_float(x[0]);
+  }
+
+  // The candidates among 32 columns starting at `col`: those above the list's
+  // worst and `bound` (exclusive); mx is the columns' maximum.  Each round every
+  // lane takes its next one.
+  __device__ static void scan32(State& S, List L, int K, float bound, const uint32_t (&r)[32],
+                                float mx, int col) {
+    const float b = fmaxf(S.kth, bound);
+    if (!__any_sync(0xffffffffu, mx > b)) return;
+    // v > b is the sign of b - v (a NaN has none): no predicates to wait for
+    uint32_t h[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 7; j >= 0; --j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[i] = __funnelshift_l(__float_as_uint(b - __uint_as_float(r[8 * i + j])), h[i], 1);
+    uint32_t hits = h[0] | h[1] << 8 | h[2] << 16 | h[3] << 24;
+    while (__any_sync(0xffffffffu, hits != 0u)) {
+      const int j = hits != 0u ? __ffs(hits) - 1 : 0;
+      const float v = pick(r, j);
+      const bool take = hits != 0u && v > S.kth;
+      hits &= hits - 1u;
+      if (__any_sync(0xffffffffu, take)) put(S, L, K, take, v, col + j);
     }
-    for (int i = 0; i < n; ++i)
-      if (qv[i] > S.kth) insert(S, p.K, qv[i], qc[i]);
+  }
+
+  // A lower bound of the K-th best of 128 columns (-inf if there are too few), by
+  // bisection between the least and the largest.  Without it the first columns
+  // of a run, which find no bound, would nearly all go through put().
+  __device__ static float first_bound(const uint32_t (&r)[4][32], int K, float mx) {
+    float lo = mx;
+#pragma unroll
+    for (int j = 0; j < 128; ++j) {
+      const float v = __uint_as_float(r[j / 32][j % 32]);
+      lo = fminf(lo, v == -CUDART_INF_F ? mx : v);
+    }
+    float hi = mx, x = lo, bound = -CUDART_INF_F;
+#pragma unroll 1
+    for (int it = 0; it < 6; ++it) {
+      uint32_t below[4] = {0u, 0u, 0u, 0u};  // v < x is the sign of v - x
+#pragma unroll
+      for (int j = 0; j < 128; ++j)
+        below[j & 3] += __float_as_uint(__uint_as_float(r[j / 32][j % 32]) - x) >> 31;
+      if (128 - static_cast<int>((below[0] + below[1]) + (below[2] + below[3])) >= K)
+        bound = lo = x;
+      else
+        hi = x;
+      x = 0.5f * lo + 0.5f * hi;
+    }
+    return bound;
   }
 
   __device__ static float max32(const uint32_t (&r)[32]) {
@@ -160,25 +252,8 @@ struct ScoreEpi {
     return mx[0];
   }
 
-  // Adds n columns (values x / scale) whose maximum is mx to the statistics.
-  template <int n>
-  __device__ static void add(Stats& st, float scale, const uint32_t (&r)[n][32], float mx) {
-    const float m1 = fmaxf(st.m, mx * scale);  // a NaN maximum (all NaN) leaves st.m
-    stats_rebase(st, m1, ex2_approx(st.m - m1));
-    float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < n * 32; ++j) {
-      const float d = max_nan(fmaf(__uint_as_float(r[j / 32][j % 32]), scale, -m1), kLowExp2);
-      const float e = ex2_approx(d);
-      s4[j & 3] += e;
-      t4[j & 3] = fmaf(e, d, t4[j & 3]);
-    }
-    st.s += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-    st.t += (t4[0] + t4[1]) + (t4[2] + t4[3]);
-  }
-
   __device__ static bool tile(const Params& p, const Pre& pre, int m_base, int col0,
-                              uint32_t taddr, int q, int lane, int part, uint8_t*,
+                              uint32_t taddr, int q, int lane, int part, uint8_t* stg,
                               const CUtensorMap*, uint32_t tempty, State& S, bool,
                               const volatile int*, unsigned long long) {
     if (col0 >= p.V) {  // the second bank of a 512-column tile past the vocabulary
@@ -187,94 +262,91 @@ struct ScoreEpi {
     }
     const int row = m_base + q * 32 + lane;
     const bool row_ok = row < p.N;
-    const int run = col0 / p.run_cols;
-    if (col0 == run * p.run_cols) {
+    const List L{reinterpret_cast<float*>(stg) + lane,
+                 reinterpret_cast<int*>(stg) + 32 * kCap + lane};
+    const int run = p.map.of_tile(col0 / p.tile_cols);
+    int run_start, run_len;
+    p.map.of_run(run, run_start, run_len);
+    const bool first = col0 == run_start * p.tile_cols;
+    if (first) {
       S.st = Stats{kNoMax, 0.f, 0.f};
-      if constexpr (kTop) {
-        S.kth = row_ok ? -CUDART_INF_F : CUDART_INF_F;  // rows past the end take nothing
-        S.told = -CUDART_INF_F;
-        for (int i = 0; i < p.K; ++i) {
-          S.lv[i] = -CUDART_INF_F;
-          S.li[i] = -1;
-        }
-      }
+      S.kth = row_ok ? -CUDART_INF_F : CUDART_INF_F;  // rows past the end take nothing
+      S.worst = 0;
+      for (int i = 0; i < p.K; ++i) L.lv[32 * i] = -CUDART_INF_F;
     }
     const int h0 = col0 + part * (BN / 2);  // this warp's first column
     const int ncols = max(0, min(BN / 2, p.V - h0));
     const uint32_t ta = taddr + part * (BN / 2);
-    if constexpr (!kSoftcap) {
-      // all 128 columns into registers, the TMEM half released at once
-      uint32_t r[4][32];
+    // all 128 columns into registers, the TMEM half released at once
+    uint32_t r[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_x32(ta + c * 32, r[c]);
-      tmem_ld_wait();
+    for (int c = 0; c < 4; ++c) tmem_ld_x32(ta + c * 32, r[c]);
+    tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) reg_fence(r[c]);
-      release_tmem(tempty, lane);
-      if (ncols < BN / 2) {  // the vocabulary ends inside (or before) these columns
+    for (int c = 0; c < 4; ++c) reg_fence(r[c]);
+    release_tmem(tempty, lane);
+    if (ncols < BN / 2) {  // the vocabulary ends inside (or before) these columns
 #pragma unroll
-        for (int j = 0; j < 128; ++j)
-          if (j >= ncols) r[j / 32][j % 32] = __float_as_uint(-CUDART_INF_F);
-      }
-      float mx[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mx[c] = max32(r[c]);
-      if constexpr (kTop) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) scan32(S, p, pre.thr, r[c], mx[c], h0 + c * 32);
-      }
-      add<4>(S.st, p.scale, r, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-    } else {
-      // softcapped: 32-column chunks, the next chunk's TMEM load in flight; the
-      // tanh body is kept rolled to bound code size
-      auto chunk = [&](int c, uint32_t(&r)[1][32]) {
-        if (c * 32 + 32 > ncols) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c * 32 + j >= ncols) r[0][j] = __float_as_uint(-CUDART_INF_F);
-        }
-        if constexpr (kTop) scan32(S, p, pre.thr, r[0], max32(r[0]), h0 + c * 32);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          r[0][j] = __float_as_uint(
-              c * 32 + j < ncols
-                  ? p.softcap * tanh_exp2(__uint_as_float(r[0][j]) * p.inv_softcap)
-                  : -CUDART_INF_F);
-        add<1>(S.st, p.scale, r, max32(r[0]));
-      };
-      constexpr int kChunks = BN / 2 / 32;
-      uint32_t b0[1][32], b1[1][32];
-      tmem_ld_x32(ta, b0[0]);
-      tmem_ld_wait(b0[0]);
-#pragma unroll 1
-      for (int c = 0; c < kChunks; c += 2) {
-        tmem_ld_x32(ta + (c + 1) * 32, b1[0]);
-        chunk(c, b0);
-        tmem_ld_wait(b1[0]);
-        if (c + 2 < kChunks)
-          tmem_ld_x32(ta + (c + 2) * 32, b0[0]);
-        else
-          release_tmem(tempty, lane);  // every column of this half is in registers
-        chunk(c + 1, b1);
-        if (c + 2 < kChunks) tmem_ld_wait(b0[0]);
-      }
+      for (int j = 0; j < 128; ++j)
+        if (j >= ncols) r[j / 32][j % 32] = __float_as_uint(-CUDART_INF_F);
     }
-    if constexpr (kTop) {
-      // tell the other runs of this row
-      S.told = fmaxf(S.told, pre.thr);
-      if (row_ok && S.kth > S.told) {
-        atomicMax(p.thr + row, order_key(S.kth));
-        S.told = S.kth;
-      }
+    float mx[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mx[c] = max32(r[c]);
+    float mx_all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+
+    // ---- list
+    // (the largest float below the rows' bound: an equal logit may still count)
+    float bound = pre.bound;
+    if (first && __any_sync(0xffffffffu, bound == -CUDART_INF_F))
+      bound = fmaxf(bound, first_bound(r, p.K, mx_all));
+    bound = nextbelow(bound);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) scan32(S, L, p.K, bound, r[c], mx[c], h0 + c * 32);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (row_ok && mx[c] > pre.bound)
+        atomicMax(p.seen + static_cast<size_t>((h0 / 32 + c) % p.K) * p.N + row,
+                  order_key(mx[c]));
+
+    // ---- statistics
+    if constexpr (kSoftcap) {
+      auto cap = [&](float z) { return p.softcap * tanh_exp2(z * p.inv_softcap); };
+#pragma unroll
+      for (int j = 0; j < 128; ++j)
+        r[j / 32][j % 32] = __float_as_uint(
+            j < ncols ? cap(__uint_as_float(r[j / 32][j % 32])) : -CUDART_INF_F);
+      // the cap keeps the order: the capped maximum is the maximum's cap (-inf: no columns)
+      mx_all = ncols > 0 ? cap(mx_all) : -CUDART_INF_F;
     }
-    const int run_end = min((run + 1) * p.run_cols, (p.V + BN - 1) / BN * BN);
+    Stats& st = S.st;
+    const float m1 = fmaxf(st.m, mx_all * p.scale);  // a NaN maximum (all NaN) leaves st.m
+    stats_rebase(st, m1, ex2_approx(st.m - m1));
+    float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 128; ++j) {
+      const float d = max_nan(fmaf(__uint_as_float(r[j / 32][j % 32]), p.scale, -m1), kLowExp2);
+      const float e = ex2_approx(d);
+      s4[j & 3] += e;
+      t4[j & 3] = fmaf(e, d, t4[j & 3]);
+    }
+    st.s += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    st.t += (t4[0] + t4[1]) + (t4[2] + t4[3]);
+
+    const int run_end = min((run_start + run_len) * p.tile_cols, (p.V + BN - 1) / BN * BN);
     if (col0 + BN >= run_end && row_ok) {  // the run's last bank
       const size_t at = static_cast<size_t>(row) * p.slots + run * 2 + part;
-      p.part[at] = make_float4(S.st.m, S.st.s, S.st.t, 0.f);
-      if constexpr (kTop) {
-        TopEntry* o = p.lists + at * p.K;
-        for (int i = 0; i < p.K; ++i) o[i] = TopEntry{S.lv[i], S.li[i]};
+      TopEntry* o = p.lists + at * p.K;
+      float best = -CUDART_INF_F;
+      int n = 0;
+      for (int i = 0; i < p.K; ++i) {
+        const TopEntry x{L.lv[32 * i], L.li[32 * i]};
+        if (x.v == -CUDART_INF_F) break;  // places are filled in order
+        best = fmaxf(best, x.v);
+        o[n++] = x;
       }
+      p.part[at] = make_float4(st.m, st.s, st.t, best);
+      p.count[at] = n;
     }
     return true;
   }
@@ -292,7 +364,8 @@ template <int kRows>
 __global__ void __launch_bounds__(kScoreThreads)
     score_simt_kernel(const float* __restrict__ hidden, const float* __restrict__ weight, int N,
                       int H, int V, float softcap, float scale, int slots, int K,
-                      float4* __restrict__ part, TopEntry* __restrict__ lists) {
+                      float4* __restrict__ part, int* __restrict__ count,
+                      TopEntry* __restrict__ lists) {
   extern __shared__ float sh[];
   float* hs = sh;               // [kRows][H]
   float* zs = sh + kRows * H;   // [kRows][kScoreCols]
@@ -353,9 +426,10 @@ __global__ void __launch_bounds__(kScoreThreads)
       st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
       st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
     }
-    if (lane == 0) part[at] = make_float4(st.m, st.s, st.t, 0.f);
     // the K largest, one after another
-    for (int i = 0; i < K; ++i) {
+    int n = 0;
+    float top = -CUDART_INF_F;
+    for (; n < K; ++n) {
       float best = -CUDART_INF_F;
       int id = -1;
       for (int c = lane; c < cols; c += 32)
@@ -372,11 +446,17 @@ __global__ void __launch_bounds__(kScoreThreads)
           id = vi;
         }
       }
+      if (id < 0) break;
+      top = fmaxf(top, best);
       if (lane == 0) {
-        lists[at * K + i] = TopEntry{best, id < 0 ? -1 : v0 + id};
-        if (id >= 0) z[id] = -CUDART_INF_F;
+        lists[at * K + n] = TopEntry{best, v0 + id};
+        z[id] = -CUDART_INF_F;
       }
       __syncwarp();
+    }
+    if (lane == 0) {
+      part[at] = make_float4(st.m, st.s, st.t, top);
+      count[at] = n;
     }
   }
 }
@@ -388,9 +468,20 @@ __global__ void __launch_bounds__(kScoreThreads)
 // of two fp32, in fp64), orders them by (logit, lowest id) and writes the row's
 // outputs at its place in token order.
 // The fp64 pass makes the order of near-equal alternatives, and with it the
-// ids, independent of how the logits were summed; it reads (top_k + margin + 1)
-// weight rows per token against the V rows of the GEMM.
+// ids, independent of how the logits were summed; it reads (K + 1) weight rows
+// per token against the V rows of the GEMM.
+// It also puts the statistics right where they are large.  The tensor cores cut
+// each of the H / 16 partial sums off towards zero, which lowers a logit of 20 at
+// H = 4096 by about 1e-4 (measured: 1e-5 of the log probability).  In the bulk of
+// the vocabulary that hardly shows (small logits), but a row whose probability
+// sits in a few tokens has an lse that is one of their logits.  So the listed
+// logits' terms are taken out of (s, t) as the epilogue added them and put back
+// with their fp64 values.  The backward recomputes the uncorrected logits: it gets
+// the uncorrected lse and entropy (`saved`), with which its 1 - p of a
+// dominant token keeps its leading digits.
 constexpr int kFinishThreads = 128;
+constexpr int kMaxHits = 512;
+constexpr int kMaxHitSlots = 256;
 
 struct FinishArgs {
   const int64_t* tokens;  // token order; null: none given
@@ -400,13 +491,16 @@ struct FinishArgs {
   int64_t ignore_index;
   float softcap;
   double inv_temp;   // 1 / temperature
-  double nat;        // 1 / (temperature * ScoreEpi's scale): see the lse below
+  double nat;        // 1 / (temperature * scale)
+  float scale;       // log2(e) / temperature in fp32, as the partial results have it
   int slots, K, top_k;
   const float4* part;
+  const int* count;
   const TopEntry* lists;
   float* logprobs;   // [N]; null without tokens
   float* entropy;    // [N]
   float* lse;        // [N]
+  float* saved;      // [2][N]: lse and entropy of the GEMM's logits
   float* top_logprobs;  // [N, top_k]
   int64_t* top_ids;     // [N, top_k]
   unsigned int* status;
@@ -437,16 +531,32 @@ __device__ __forceinline__ double dot_part(const float* a, const float* b, int H
   return acc;
 }
 
+// The softcap as the partial results have it.
+template <class T>
+__device__ __forceinline__ float gemm_softcap(float z, float softcap);
+template <>
+__device__ __forceinline__ float gemm_softcap<__nv_bfloat16>(float z, float softcap) {
+  return softcap * tanh_exp2(z * (1.0f / softcap));
+}
+template <>
+__device__ __forceinline__ float gemm_softcap<float>(float z, float softcap) {
+  return capped(z, softcap);
+}
+
 template <class T>
 __global__ void __launch_bounds__(kFinishThreads)
     score_finish_kernel(const T* __restrict__ hidden, const T* __restrict__ weight,
                         const FinishArgs a) {
   constexpr int kWarps = kFinishThreads / 32;
   __shared__ Stats wst[kWarps];
-  __shared__ float bv[2][kWarps];
-  __shared__ int bi[2][kWarps], bt[2][kWarps];
+  __shared__ float tmaxs[kFinishThreads], bound_sh;
+  __shared__ int n_hits, n_hit_slots;
+  __shared__ int hit_slots[kMaxHitSlots];  // slot, and its entries in the top byte
+  __shared__ TopEntry hits[kMaxHits], wbest[2][kWarps];
   __shared__ int ids[kMaxTopList + 1];
+  __shared__ float za[kMaxTopList];
   __shared__ double zx[kMaxTopList + 1];
+  __shared__ double lse_sh;
   griddep_wait();
   const int j = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int row = a.perm != nullptr ? a.perm[j] : j;
@@ -463,6 +573,8 @@ __global__ void __launch_bounds__(kFinishThreads)
       if (a.logprobs != nullptr) a.logprobs[row] = 0.f;
       a.entropy[row] = 0.f;
       a.lse[row] = 0.f;
+      a.saved[row] = 0.f;
+      a.saved[a.N + row] = 0.f;
     }
     for (int i = t; i < a.top_k; i += kFinishThreads) {
       a.top_logprobs[static_cast<size_t>(row) * a.top_k + i] = 0.f;
@@ -471,11 +583,16 @@ __global__ void __launch_bounds__(kFinishThreads)
     return;
   }
 
-  // ---- statistics
+  // ---- statistics, and the largest entry of this thread's lists
+  const float4* part = a.part + static_cast<size_t>(j) * a.slots;
+  const int* count = a.count + static_cast<size_t>(j) * a.slots;
+  const TopEntry* lists = a.lists + static_cast<size_t>(j) * a.slots * a.K;
   Stats st{kNoMax, 0.f, 0.f};
+  float tmax = -CUDART_INF_F;
   for (int i = t; i < a.slots; i += kFinishThreads) {
-    const float4 v = a.part[static_cast<size_t>(j) * a.slots + i];
+    const float4 v = part[i];
     stats_merge(st, Stats{v.x, v.y, v.z});
+    tmax = fmaxf(tmax, v.w);
   }
 #pragma unroll
   for (int o = 16; o >= 1; o /= 2)
@@ -484,67 +601,85 @@ __global__ void __launch_bounds__(kFinishThreads)
                           __shfl_down_sync(0xffffffffu, st.t, o)});
   if (lane == 0) wst[warp] = st;
 
-  // ---- the K best entries: every thread keeps the best head of its lists
-  if (a.K > 0) {
-    const TopEntry* L = a.lists + static_cast<size_t>(j) * a.slots * a.K;
-    // heads of the lists t, t + kFinishThreads, ...: an entry is taken by its
-    // thread at most once, in list order, so a position per list would do; the
-    // thread's last taken (value, id) says the same for all its lists
-    float last_v = CUDART_INF_F;
-    int last_id = -1;
+  // ---- the K best entries.  The K-th largest of the threads' maxima is a lower
+  // bound of the K-th best (each is an entry of its own), and about K lists have
+  // entries that reach it.  Those entries are ranked against one another; if
+  // ties make them more than fit, the K best are taken one by one from all lists.
+  tmaxs[t] = tmax;
+  if (t == 0) {
+    n_hits = n_hit_slots = 0;
+    bound_sh = -CUDART_INF_F;
+  }
+  if (t <= a.K) ids[t] = -1;
+  __syncthreads();
+  {
+    int above = 0, ties = 0;
+#pragma unroll 8
+    for (int i = 0; i < kFinishThreads; ++i) {
+      above += tmaxs[i] > tmax ? 1 : 0;
+      ties += tmaxs[i] == tmax ? 1 : 0;
+    }
+    if (above < a.K && above + ties >= a.K) bound_sh = tmax;  // one value whoever writes it
+  }
+  __syncthreads();
+  const float bound = bound_sh;
+  if (tmax >= bound && tmax > -CUDART_INF_F)
+    for (int l = t; l < a.slots; l += kFinishThreads)
+      if (part[l].w >= bound && count[l] > 0) {
+        const int at = atomicAdd(&n_hit_slots, 1);
+        if (at < kMaxHitSlots) hit_slots[at] = l | count[l] << 24;
+      }
+  __syncthreads();
+  if (n_hit_slots <= kMaxHitSlots) {
+    for (int e = t; e < n_hit_slots * a.K; e += kFinishThreads) {
+      const int h = e / a.K, i = e - h * a.K;
+      const int l = hit_slots[h] & 0xffffff;
+      if (i >= hit_slots[h] >> 24) continue;
+      const TopEntry x = lists[static_cast<size_t>(l) * a.K + i];
+      if (x.v >= bound) {
+        const int at = atomicAdd(&n_hits, 1);
+        if (at < kMaxHits) hits[at] = x;
+      }
+    }
+  }
+  __syncthreads();
+  if (n_hit_slots <= kMaxHitSlots && n_hits <= kMaxHits) {
+    for (int i = t; i < n_hits; i += kFinishThreads) {
+      const TopEntry x = hits[i];
+      int rank = 0;
+      for (int c = 0; c < n_hits && rank < a.K; ++c) rank += better(hits[c], x) ? 1 : 0;
+      if (rank < a.K) {
+        ids[rank] = x.id;
+        za[rank] = x.v;
+      }
+    }
+  } else {
+    TopEntry last{CUDART_INF_F, -1};  // taken last: the order's place to go on from
     for (int n = 0; n < a.K; ++n) {
-      float best = -CUDART_INF_F;
-      int id = -1;
+      TopEntry best{-CUDART_INF_F, -1};
       for (int l = t; l < a.slots; l += kFinishThreads) {
-        const TopEntry* e = L + static_cast<size_t>(l) * a.K;
-        for (int i = 0; i < a.K; ++i) {
+        const TopEntry* e = lists + static_cast<size_t>(l) * a.K;
+        for (int i = 0; i < count[l]; ++i) {
           const TopEntry x = e[i];
-          if (x.id < 0) break;
-          // not taken yet: behind (last_v, last_id) in the order
-          if (x.v < last_v || (x.v == last_v && x.id > last_id)) {
-            if (id < 0 || x.v > best || (x.v == best && x.id < id)) {
-              best = x.v;
-              id = x.id;
-            }
-            break;
-          }
+          if (better(last, x) && (best.id < 0 || better(x, best))) best = x;
         }
       }
-      int who = t;
+      auto take = [&](TopEntry x) {
+        if (x.id >= 0 && (best.id < 0 || better(x, best))) best = x;
+      };
 #pragma unroll
-      for (int o = 16; o >= 1; o /= 2) {
-        const float v = __shfl_xor_sync(0xffffffffu, best, o);
-        const int vi = __shfl_xor_sync(0xffffffffu, id, o);
-        const int vw = __shfl_xor_sync(0xffffffffu, who, o);
-        if (vi >= 0 && (id < 0 || v > best || (v == best && vi < id))) {
-          best = v;
-          id = vi;
-          who = vw;
-        }
-      }
-      if (lane == 0) {
-        bv[n & 1][warp] = best;
-        bi[n & 1][warp] = id;
-        bt[n & 1][warp] = who;
-      }
+      for (int o = 16; o >= 1; o /= 2)
+        take(TopEntry{__shfl_xor_sync(0xffffffffu, best.v, o),
+                      __shfl_xor_sync(0xffffffffu, best.id, o)});
+      if (lane == 0) wbest[n & 1][warp] = best;
       __syncthreads();
-      float gv = bv[n & 1][0];
-      int gi = bi[n & 1][0], gw = bt[n & 1][0];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        const float v = bv[n & 1][w];
-        const int vi = bi[n & 1][w];
-        if (vi >= 0 && (gi < 0 || v > gv || (v == gv && vi < gi))) {
-          gv = v;
-          gi = vi;
-          gw = bt[n & 1][w];
-        }
+      for (int w = 0; w < kWarps; ++w) take(wbest[n & 1][w]);
+      last = best;
+      if (t == 0) {
+        ids[n] = best.id;
+        za[n] = best.v;
       }
-      if (t == gw && gi >= 0) {
-        last_v = gv;
-        last_id = gi;
-      }
-      if (t == 0) ids[n] = gi;
     }
   }
   if (t == 0) ids[a.K] = a.tokens != nullptr ? static_cast<int>(y) : -1;
@@ -565,22 +700,66 @@ __global__ void __launch_bounds__(kFinishThreads)
   __syncthreads();
 
   // ---- outputs
-  st = wst[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) stats_merge(st, wst[w]);
   const double ln2 = 0.693147180559945309417;
-  const double log2_s = st.s == 0.f ? -CUDART_INF : log2(static_cast<double>(st.s));
-  // the maximum goes back by the fp32 scale that made it, so the rounding of
-  // log2(e) / temperature does not reach the lse through it
-  const double lse = static_cast<double>(st.m) * a.nat + ln2 * log2_s;
-  auto logprob = [&](double z) -> float {
-    const double L = a.softcap > 0.f ? a.softcap * tanh(z / a.softcap) : z;
-    return static_cast<float>(L * a.inv_temp - lse);
-  };
-  if (t == 0) {
-    a.lse[row] = static_cast<float>(lse);
-    a.entropy[row] = static_cast<float>(ln2 * (log2_s - static_cast<double>(st.t) / st.s));
+  auto capped64 = [&](double z) { return a.softcap > 0.f ? a.softcap * tanh(z / a.softcap) : z; };
+  if (warp == 0) {
+    st = wst[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) stats_merge(st, wst[w]);
+    auto sum = [](double v) {
+#pragma unroll
+      for (int o = 16; o >= 1; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    };
+    // log2-domain values of the listed logits, from the GEMM (xa) and in fp64 (xe)
+    const double to_log2 = a.inv_temp / ln2;
+    const double M = st.m, Me = M * a.nat / ln2;  // in the fp32 scale's units; exactly
+    double s_rest = 0.0, t_rest = 0.0, m1 = Me;
+    for (int c = lane; c < a.K; c += 32) {
+      if (ids[c] < 0) continue;
+      const float L = a.softcap > 0.f ? gemm_softcap<T>(za[c], a.softcap) : za[c];
+      const double da = fmax(static_cast<double>(L) * a.scale - M, double(kLowExp2));
+      const double e = exp2(da);
+      s_rest += e;
+      t_rest += e * da;
+      m1 = fmax(m1, capped64(zx[c]) * to_log2);
+    }
+    s_rest = sum(s_rest);
+    t_rest = sum(t_rest);
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    // what the listed ones leave (a NaN sum stays NaN), at the new maximum
+    s_rest = st.s - s_rest;
+    t_rest = st.t - t_rest;
+    if (s_rest < 0.0) s_rest = 0.0;
+    if (t_rest > 0.0) t_rest = 0.0;
+    const double down = exp2(Me - m1);
+    double s1 = 0.0, t1 = 0.0;
+    for (int c = lane; c < a.K; c += 32) {
+      if (ids[c] < 0) continue;
+      const double de = fmax(capped64(zx[c]) * to_log2 - m1, double(kLowExp2));
+      const double e = exp2(de);
+      s1 += e;
+      t1 += e * de;
+    }
+    s1 = sum(s1) + s_rest * down;
+    t1 = sum(t1) + (t_rest + s_rest * (Me - m1)) * down;
+    if (lane == 0) {
+      const double log2_s = s1 == 0.0 ? -CUDART_INF : log2(s1);
+      const double lse = ln2 * (m1 + log2_s);
+      lse_sh = lse;
+      a.lse[row] = static_cast<float>(lse);
+      a.entropy[row] = static_cast<float>(ln2 * (log2_s - t1 / s1));
+      const double log2_a = st.s == 0.f ? -CUDART_INF : log2(static_cast<double>(st.s));
+      a.saved[row] = static_cast<float>(M * a.nat + ln2 * log2_a);
+      a.saved[a.N + row] = static_cast<float>(ln2 * (log2_a - static_cast<double>(st.t) / st.s));
+    }
   }
+  __syncthreads();
+  const double lse = lse_sh;
+  auto logprob = [&](double z) -> float {
+    return static_cast<float>(capped64(z) * a.inv_temp - lse);
+  };
   if (t == 32 && a.logprobs != nullptr) a.logprobs[row] = logprob(zx[a.K]);
   if (t < a.K) {
     const int id = ids[t];

@@ -21,18 +21,16 @@ constexpr int kMaxRun = 16;
 struct ScorePlan {
   int cta_group;   // 1: 128 x 256 tiles of single CTAs, 2: 256-row tiles of pairs
   int bn;          // columns of a tile
-  int run;         // column tiles of a run
+  RunMap map;      // runs of column tiles
+  int runs;
   int slots;       // partial results per row
-  int K;           // list length (0: no alternatives)
+  int K;           // list length
   bool compact;    // rows without a token are left out of the GEMM
 };
 
-// Runs are as long as an even spread over the SMs allows: of the run lengths up
-// to kMaxRun the one with the least time in units of tiles, ceil(runs / workers)
-// * run, and of equal ones the longest (fewest partial results).
 ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k) {
   ScorePlan P{};
-  P.K = top_k > 0 ? static_cast<int>(std::min<int64_t>(top_k + kTopMargin, V)) : 0;
+  P.K = static_cast<int>(std::min<int64_t>(std::max(top_k + kTopMargin, kMinTopList), V));
   if (!bf16) {
     P.slots = static_cast<int>((V + kScoreCols - 1) / kScoreCols);
     return P;
@@ -41,34 +39,36 @@ ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k) 
   P.bn = P.cta_group == 1 ? 256 : o.fwd_bn;
   P.compact = N > kFewRows && o.fwd_compact;
   const int64_t unit_rows = BM * P.cta_group, workers = kPlanSms / P.cta_group;
-  const int64_t mt = (N + unit_rows - 1) / unit_rows, nt = (V + P.bn - 1) / P.bn;
-  int64_t best = INT64_MAX;
-  for (int r = 1; r <= kMaxRun && r <= nt; ++r) {
-    const int64_t runs = mt * ((nt + r - 1) / r);
-    const int64_t time = (runs + workers - 1) / workers * r;
-    if (time <= best) {
-      best = time;
-      P.run = r;
-    }
-  }
-  P.slots = static_cast<int>(2 * ((nt + P.run - 1) / P.run));
+  const int64_t mt = std::max<int64_t>((N + unit_rows - 1) / unit_rows, 1);
+  const int64_t nt = (V + P.bn - 1) / P.bn;
+  // the longest runs: a power of two, four for every worker; then run_q (one for
+  // every worker) of each smaller length
+  int64_t n = 1;
+  while (n < kMaxRun && 2 * n * 4 * workers <= mt * nt) n *= 2;
+  const int64_t q = (workers + mt - 1) / mt;
+  const int64_t c0 = n == 1 ? nt : std::max<int64_t>(0, (nt - q * (n - 1)) / n);
+  P.map = RunMap{static_cast<int>(n), static_cast<int>(c0), static_cast<int>(q)};
+  P.runs = P.map.of_tile(static_cast<int>(nt - 1)) + 1;
+  P.slots = 2 * P.runs;
   return P;
 }
 
-// Workspace: header | row bounds (zeroed with the header) | statistics | lists |
+// Workspace: header | group maxima (zeroed with the header) | statistics | lists |
 // row compaction.
 struct ScoreLayout {
-  size_t thr, part, lists, perm, tokens_c, block_valid, n_valid_c, hidden_c, end;
+  size_t seen, part, count, lists, perm, tokens_c, block_valid, n_valid_c, hidden_c, end;
 };
 
 ScoreLayout score_layout(const ScorePlan& P, int64_t N, int64_t H) {
   ScoreLayout L{};
   const size_t n = static_cast<size_t>(N);
   size_t off = kHeaderBytes;
-  L.thr = off;
-  off = align_up(off + 4 * n, 256);
+  L.seen = off;
+  off = align_up(off + 4 * n * P.K, 256);
   L.part = off;
   off = align_up(off + sizeof(float4) * n * P.slots, 256);
+  L.count = off;
+  off = align_up(off + sizeof(int) * n * P.slots, 256);
   L.lists = off;
   off = align_up(off + sizeof(TopEntry) * n * P.slots * P.K, 256);
   if (P.compact) {
@@ -92,6 +92,7 @@ bool score_sizes_ok(int64_t N, int64_t H, int64_t V, int32_t dtype) {
   if (N < 0 || V < 1 || H < 8 || N > kMaxDim || V > kMaxDim || H > kMaxDim) return false;
   if (dtype == FLCE_BF16 ? H % 8 != 0 : H > kSimtMaxH) return false;
   if (((N + BM - 1) / BM) * ((V + BN - 1) / BN) > (int64_t{1} << 26)) return false;
+  if ((V + BN - 1) / BN >= (1 << 22)) return false;  // (a row's slots are counted in 24 bits)
   return dtype == FLCE_BF16 || (N + 1) / 2 <= 65535;  // score_simt's grid
 }
 
@@ -133,7 +134,7 @@ cudaError_t run_finish(const void* hidden, const void* weight, const FinishArgs&
 
 flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout& L,
                        const void* hidden, const void* weight, const int64_t* tokens,
-                       FinishArgs fin, float scale, char* w, cudaStream_t st) {
+                       FinishArgs fin, char* w, cudaStream_t st) {
   const int n = fin.N, H = fin.H;
   const void* hid = hidden;
   long long* n_valid_c = nullptr;
@@ -184,7 +185,10 @@ flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout
   g.status = fin.status;
   g.timeout_ns = o.timeout_ns;
   g.tile_counter = o.fwd_dynamic ? ws_fwd_counter(w) : nullptr;
-  g.run_n = P.run;
+  g.run_n = P.map.n;
+  g.run_c0 = P.map.c0;
+  g.run_q = P.map.q;
+  g.runs = P.runs;
   if (n_valid_c != nullptr) {
     g.rows_valid = n_valid_c;
     g.rows_host = n;
@@ -197,19 +201,23 @@ flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout
                                   fin.V,
                                   fin.softcap,
                                   fin.softcap > 0.f ? 1.0f / fin.softcap : 0.f,
-                                  scale,
-                                  P.run * P.bn,
+                                  fin.scale,
+                                  P.map,
+                                  P.bn,
                                   P.slots,
                                   P.K,
                                   reinterpret_cast<float4*>(w + L.part),
+                                  reinterpret_cast<int*>(w + L.count),
                                   reinterpret_cast<TopEntry*>(w + L.lists),
-                                  reinterpret_cast<uint32_t*>(w + L.thr)};
+                                  reinterpret_cast<uint32_t*>(w + L.seen)};
     return run_gemm<Epi, false, false>(d, o, P.bn, kFwdGemm, prob, ep, nullptr, ep, st);
   };
-  if (P.K > 0)
-    e = fin.softcap > 0.f ? score(ScoreEpi<true, true>{}) : score(ScoreEpi<false, true>{});
+  if (P.K <= kSmallTopList)
+    e = fin.softcap > 0.f ? score(ScoreEpi<true, kSmallTopList>{})
+                          : score(ScoreEpi<false, kSmallTopList>{});
   else
-    e = fin.softcap > 0.f ? score(ScoreEpi<true, false>{}) : score(ScoreEpi<false, false>{});
+    e = fin.softcap > 0.f ? score(ScoreEpi<true, kMaxTopList>{})
+                          : score(ScoreEpi<false, kMaxTopList>{});
   if (e == cudaSuccess) e = run_finish<__nv_bfloat16>(hidden, weight, fin, st);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
 }
@@ -223,7 +231,7 @@ size_t score_simt_smem(int rows, int64_t H) {
 
 template <int kRows>
 cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishArgs& a,
-                           float scale, float4* part, TopEntry* lists, cudaStream_t st) {
+                           float4* part, int* count, TopEntry* lists, cudaStream_t st) {
   static_assert(2 * (kSimtMaxH + kScoreCols) * sizeof(float) <= kScoreSimtSmem, "two rows fit");
   const cudaError_t e = set_smem_attr(score_simt_kernel<kRows>, kScoreSimtSmem);
   if (e != cudaSuccess) return e;
@@ -231,7 +239,7 @@ cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishA
   return launch(kSimt, st, [&] {
     score_simt_kernel<kRows><<<grid, kScoreThreads, score_simt_smem(kRows, a.H), st>>>(
         static_cast<const float*>(hidden), static_cast<const float*>(weight), a.N, a.H, a.V,
-        a.softcap, scale, a.slots, a.K, part, lists);
+        a.softcap, a.scale, a.slots, a.K, part, count, lists);
   });
 }
 
@@ -253,7 +261,7 @@ size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dt
 flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,
                                   int64_t N, int64_t H, int64_t V, int64_t ignore_index,
                                   float softcap, double temperature, int32_t top_k, int32_t dtype,
-                                  float* logprobs, float* entropy, float* lse,
+                                  float* logprobs, float* entropy, float* lse, float* saved,
                                   float* top_logprobs, int64_t* top_ids, void* workspace,
                                   size_t workspace_bytes, void* stream) {
   static_assert(FLCE_MAX_TOP_K == kMaxTopK, "header and kernels agree");
@@ -264,7 +272,7 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   if ((reinterpret_cast<uintptr_t>(tokens) & 7u) != 0 ||
       (reinterpret_cast<uintptr_t>(top_ids) & 7u) != 0)
     return FLCE_ERR_ARG;
-  if (N > 0 && (entropy == nullptr || lse == nullptr)) return FLCE_ERR_ARG;
+  if (N > 0 && (entropy == nullptr || lse == nullptr || saved == nullptr)) return FLCE_ERR_ARG;
   if (N > 0 && (tokens == nullptr) != (logprobs == nullptr)) return FLCE_ERR_ARG;
   if (N > 0 && top_k > 0 && (top_logprobs == nullptr || top_ids == nullptr)) return FLCE_ERR_ARG;
   const bool bf16 = dtype == FLCE_BF16;
@@ -276,8 +284,9 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   if (s != FLCE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(workspace);
-  // status word and tile counter, and the rows' bounds behind them
-  cudaError_t e = cudaMemsetAsync(w, 0, P.K > 0 ? L.thr + 4 * static_cast<size_t>(N) : 16, st);
+  // status word and tile counter, and the group maxima behind them
+  cudaError_t e =
+      cudaMemsetAsync(w, 0, L.seen + (bf16 ? 4 * static_cast<size_t>(N) * P.K : 0), st);
   if (e != cudaSuccess) return cuda_fail(e);
   if (N == 0) return FLCE_OK;
   const float scale = static_cast<float>(1.4426950408889634074 / temperature);
@@ -289,40 +298,44 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   fin.ignore_index = ignore_index;
   fin.softcap = softcap;
   fin.inv_temp = 1.0 / temperature;
+  fin.scale = scale;
   fin.nat = 1.0 / (temperature * static_cast<double>(scale));
   fin.slots = P.slots;
   fin.K = P.K;
   fin.top_k = top_k;
   fin.part = reinterpret_cast<const float4*>(w + L.part);
+  fin.count = reinterpret_cast<const int*>(w + L.count);
   fin.lists = reinterpret_cast<const TopEntry*>(w + L.lists);
   fin.logprobs = logprobs;
   fin.entropy = entropy;
   fin.lse = lse;
+  fin.saved = saved;
   fin.top_logprobs = top_logprobs;
   fin.top_ids = top_ids;
   fin.status = ws_status(w);
-  if (bf16) return score_bf16(d, o, P, L, hidden, weight, tokens, fin, scale, w, st);
+  if (bf16) return score_bf16(d, o, P, L, hidden, weight, tokens, fin, w, st);
   float4* part = reinterpret_cast<float4*>(w + L.part);
+  int* count = reinterpret_cast<int*>(w + L.count);
   TopEntry* lists = reinterpret_cast<TopEntry*>(w + L.lists);
   e = score_simt_smem(8, H) <= kScoreSimtSmem
-          ? run_score_simt<8>(hidden, weight, fin, scale, part, lists, st)
-          : run_score_simt<2>(hidden, weight, fin, scale, part, lists, st);
+          ? run_score_simt<8>(hidden, weight, fin, part, count, lists, st)
+          : run_score_simt<2>(hidden, weight, fin, part, count, lists, st);
   if (e == cudaSuccess) e = run_finish<float>(hidden, weight, fin, st);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
 }
 
 flce_status flce_logprobs_backward(const void* hidden, const void* weight, const int64_t* tokens,
-                                   const float* lse, const float* entropy, int64_t N, int64_t H,
-                                   int64_t V, int64_t ignore_index, float softcap,
-                                   double temperature, int32_t dtype, const float* d_logprobs,
-                                   const float* d_entropy, float* d_hidden, float* d_weight,
-                                   int32_t flags, void* workspace, size_t workspace_bytes,
-                                   void* stream) {
+                                   const float* saved, int64_t N, int64_t H, int64_t V,
+                                   int64_t ignore_index, float softcap, double temperature,
+                                   int32_t dtype, const float* d_logprobs, const float* d_entropy,
+                                   float* d_hidden, float* d_weight, int32_t flags,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
   if (!(temperature >= 1e-30) || !(temperature <= 1e30)) return FLCE_ERR_ARG;
-  if (d_entropy != nullptr && N > 0 && entropy == nullptr) return FLCE_ERR_ARG;
-  const RowGrads rg{d_logprobs, d_entropy, entropy, static_cast<float>(1.0 / temperature)};
-  return backward_any(hidden, weight, tokens, lse, N, H, V, ignore_index, softcap, FLCE_SUM, dtype,
-                      nullptr, 1.0f, -1, nullptr, d_hidden, d_weight, flags, workspace,
+  // (saved: lse of every row, then entropy; a null one is refused like a null lse)
+  const RowGrads rg{d_logprobs, d_entropy, saved != nullptr && N > 0 ? saved + N : nullptr,
+                    static_cast<float>(1.0 / temperature)};
+  return backward_any(hidden, weight, tokens, saved, N, H, V, ignore_index, softcap, FLCE_SUM,
+                      dtype, nullptr, 1.0f, -1, nullptr, d_hidden, d_weight, flags, workspace,
                       workspace_bytes, stream, &rg);
 }
 

@@ -62,7 +62,12 @@ constexpr int kABytes = BM * BK * 2;  // 16 KB
 constexpr int kStagingBuf = 4096;                 // 32 rows x 128 bytes
 constexpr uint32_t kTmemCols = 512;
 
-template <int kCG, int kBN = 256>
+// Largest dynamic shared memory of a GEMM CTA (static shared memory aside).
+constexpr size_t kMaxGemmSmem = 227 * 1024 - 512;
+
+// kEpiBytes: shared memory of the epilogue; more than the usual staging buffers
+// leave room for costs stages.
+template <int kCG, int kBN = 256, size_t kEpiBytes = 0>
 struct TileCfg {
   static_assert(kBN == 256 || (kBN == 512 && kCG == 2), "512-column tiles need CTA pairs");
   static constexpr int kBanks = kBN / BN;          // 256-column TMEM banks of one tile
@@ -71,7 +76,11 @@ struct TileCfg {
   static constexpr int kBRows = kBanks * kBankRows;  // B rows (N index) staged by one CTA
   static constexpr int kBBytes = kBRows * BK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = (kCG == 1 || kBN == 512) ? 4 : 6;
+  static constexpr int kMostStages = (kCG == 1 || kBN == 512) ? 4 : 6;
+  static constexpr int kFitStages =
+      static_cast<int>((kMaxGemmSmem - 1024 - kEpiBytes) / kStageBytes);
+  static constexpr int kStages = kFitStages < kMostStages ? kFitStages : kMostStages;
+  static_assert(kStages >= 3, "stages of the operand ring");
   static constexpr int kUnitRows = BM * kCG;  // output rows of one tile
   static constexpr size_t kRingBytes = 1024 + static_cast<size_t>(kStages) * kStageBytes;
 };
@@ -82,10 +91,15 @@ template <class Epi>
 constexpr int gemm_threads() {
   return 64 + 32 * Epi::kEpiWarps;
 }
+template <class Epi>
+constexpr size_t epi_smem_bytes() {
+  return static_cast<size_t>(Epi::kEpiWarps) * Epi::kStagingPerWarp;
+}
+template <class Epi, int kCG, int kBN>
+using EpiTileCfg = TileCfg<kCG, kBN, epi_smem_bytes<Epi>()>;
 template <class Epi, int kCG, int kBN>
 constexpr size_t gemm_smem_bytes() {
-  return TileCfg<kCG, kBN>::kRingBytes +
-         static_cast<size_t>(Epi::kEpiWarps) * Epi::kStagingPerWarp;
+  return EpiTileCfg<Epi, kCG, kBN>::kRingBytes + epi_smem_bytes<Epi>();
 }
 
 constexpr int kRing = 8;  // tile indices in flight between the fetcher and the other roles
@@ -148,8 +162,9 @@ struct GemmArgs {
   // TMA requests: 76.7 vs 68.9 B/clk per SM measured into shared memory.
   int a_mn3d, b_mn3d;
   // Epilogues that carry a row's state from tile to tile (Epi::kRun): tiles are
-  // handed out in runs of up to run_n consecutive column tiles of one row tile.
-  int run_n;
+  // handed out in runs of consecutive column tiles of one row tile, `runs` per
+  // row tile, cut as RunMap{run_n, run_c0, run_q} says.
+  int run_n, run_c0, run_q, runs;
 };
 
 constexpr int kRowsNone = 0;
@@ -171,18 +186,54 @@ __device__ __forceinline__ void tile_coords(int tile, const GemmArgs& g, int& mb
   nb = r / gm;
 }
 
-// The same for runs of run_n column tiles (tile index = run * run_n + position
-// in the run): runs are walked in the raster order of tile_coords.
-__device__ __forceinline__ void run_tile_coords(int tile, const GemmArgs& g, int& mb, int& nb) {
-  const int run = tile / g.run_n;
-  const int runs_n = (g.n_tiles + g.run_n - 1) / g.run_n;
-  const int per_group = g.group_m * runs_n;
+// Cuts the column tiles of a row tile into runs: run_c0 runs of run_n tiles (a
+// power of two), then run_q runs of each smaller power of two and single tiles
+// to the end.  Long runs carry a row's state far; the short ones come last, so
+// that the SMs finish together however many row tiles there are.
+struct RunMap {
+  int n, c0, q;
+  __host__ __device__ void of_run(int run, int& start, int& len) const {
+    if (run < c0) {
+      start = run * n;
+      len = n;
+      return;
+    }
+    start = c0 * n;
+    run -= c0;
+    for (len = n > 1 ? n / 2 : 1; len > 1 && run >= q; len /= 2) {
+      start += q * len;
+      run -= q;
+    }
+    start += run * len;
+  }
+  __host__ __device__ int of_tile(int tile) const {
+    if (tile < c0 * n) return tile / n;
+    int run = c0, len;
+    tile -= c0 * n;
+    for (len = n > 1 ? n / 2 : 1; len > 1 && tile >= q * len; len /= 2) {
+      tile -= q * len;
+      run += q;
+    }
+    return run + tile / len;
+  }
+};
+
+// tile_coords for runs: tile index = run_n * (run in raster order) + position in
+// the run; `left` receives the tiles from here to the run's end.
+__device__ __forceinline__ void run_tile_coords(int tile, const GemmArgs& g, int& mb, int& nb,
+                                                int& left) {
+  const RunMap map{g.run_n, g.run_c0, g.run_q};
+  const int run = tile / g.run_n, pos = tile - run * g.run_n;
+  const int per_group = g.group_m * g.runs;
   const int grp = run / per_group;
   const int first_m = grp * g.group_m;
   const int gm = min(g.group_m, g.m_tiles - first_m);
   const int r = run - grp * per_group;
   mb = first_m + r % gm;
-  nb = (r / gm) * g.run_n + (tile - run * g.run_n);
+  int start, len;
+  map.of_run(r / gm, start, len);
+  nb = start + pos;
+  left = min(len, g.n_tiles - start) - pos;
 }
 
 // Hand the accumulator back to the MMA issuer: `tempty_bar` is the
@@ -765,7 +816,7 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
                    const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmOut1,
                    const GemmArgs g0, const GemmArgs g1, const typename Epi::Params ep0,
                    const typename Epi::Params ep1) {
-  using Cfg = TileCfg<kCG, kBN>;
+  using Cfg = EpiTileCfg<Epi, kCG, kBN>;
   static_assert(Epi::kEpiWarps == 8, "two epilogue warps per TMEM lane quadrant, half a bank each");
   constexpr int kStages = Cfg::kStages;
   constexpr int kBanks = Cfg::kBanks;
@@ -856,9 +907,7 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
   const GemmArgs a0 = bound_rows(g0);
   const GemmArgs a1 = bound_rows(g1);
   // (runs: one problem, every run counted as run_n tile indices)
-  const int tiles0 = Epi::kRun
-      ? a0.m_tiles * ((a0.n_tiles + a0.run_n - 1) / a0.run_n) * a0.run_n
-      : a0.m_tiles * a0.n_tiles;
+  const int tiles0 = Epi::kRun ? a0.m_tiles * a0.runs * a0.run_n : a0.m_tiles * a0.n_tiles;
   const int num_tiles = Epi::kRun ? tiles0 : tiles0 + a1.m_tiles * a1.n_tiles;
   const int unit = blockIdx.x / kCG;  // CTA (kCG = 1) or CTA pair (kCG = 2)
   const int n_units = gridDim.x / kCG;
@@ -867,8 +916,9 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
   // problem, its args and the tile's coordinates for global tile index t
   auto locate = [&](int t, int& prob, int& mb, int& nb) {
     if constexpr (Epi::kRun) {
+      int left;
       prob = 0;
-      run_tile_coords(t, a0, mb, nb);
+      run_tile_coords(t, a0, mb, nb, left);
       return;
     }
     prob = (t < tiles0) ? 0 : 1;
@@ -933,10 +983,10 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
                                                            : unit + k * n_units;
               // (run < num_tiles first: the product must not wrap past the last run)
               if (run < num_tiles && run * a0.run_n < num_tiles) {
-                int mb, nb;
-                run_tile_coords(run * a0.run_n, a0, mb, nb);
+                int mb, nb, left;
                 run_next = run * a0.run_n;
-                run_end = run_next + min(a0.run_n, a0.n_tiles - nb);
+                run_tile_coords(run_next, a0, mb, nb, left);
+                run_end = run_next + left;
               } else {
                 run_next = num_tiles;
                 run_end = num_tiles + 1;

@@ -5,8 +5,8 @@ CUDA library, see flce_logprobs_forward in include/flce.h).
 
   logprobs_forward(hidden, weight, tokens=None, ignore_index=-100, softcap=0.0,
                    temperature=1.0, top_k=0)
-      -> Logprobs(logprobs, entropy, lse, top_logprobs, top_ids)
-  logprobs_backward(hidden, weight, tokens, lse, entropy, d_logprobs, d_entropy)
+      -> Logprobs(logprobs, entropy, lse, top_logprobs, top_ids, saved)
+  logprobs_backward(hidden, weight, tokens, saved, d_logprobs, d_entropy)
       -> (d_hidden, d_weight)
   fused_linear_logprobs(...)  the differentiable form: gradients of the log
       probabilities and the entropy flow to hidden and weight
@@ -28,6 +28,7 @@ class Logprobs(NamedTuple):
     lse: torch.Tensor                     # float32 [...]
     top_logprobs: Optional[torch.Tensor]  # float32 [..., top_k]; None with top_k=0
     top_ids: Optional[torch.Tensor]       # int64 [..., top_k]
+    saved: torch.Tensor                   # float32 [2, N]: logprobs_backward's
 
 
 def logprobs_workspace_bytes(N: int, H: int, V: int, dtype: torch.dtype = torch.bfloat16,
@@ -63,20 +64,21 @@ def logprobs_forward(hidden: torch.Tensor, weight: torch.Tensor,
     else:
         check_workspace(workspace, dev)
     # one allocation for the float outputs of a row
-    f = torch.empty((2 if y is None else 3, N), dtype=torch.float32, device=dev)
+    f = torch.empty((4 if y is None else 5, N), dtype=torch.float32, device=dev)
     top_lp = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
     top_ids = torch.empty((N, k), dtype=torch.int64, device=dev) if k else None
     with on_device(dev):
         st = _lib().flce_logprobs_forward(
             _ptr(h2), _ptr(w), _ptr(y), N, H, V, int(ignore_index), float(softcap),
-            float(temperature), k, _DTYPES[h2.dtype], None if y is None else _ptr(f[2]),
-            _ptr(f[0]), _ptr(f[1]), _ptr(top_lp), _ptr(top_ids), _ptr(workspace),
+            float(temperature), k, _DTYPES[h2.dtype], None if y is None else _ptr(f[4]),
+            _ptr(f[2]), _ptr(f[3]), _ptr(f), _ptr(top_lp), _ptr(top_ids), _ptr(workspace),
             workspace.numel(), _stream(dev))
     _native.check(st, "flce_logprobs_forward")
     if check_status:
         _native.check(status(workspace), "flce_logprobs_forward (device status)")
-    return Logprobs(None if y is None else f[2].view(lead), f[0].view(lead), f[1].view(lead),
-                    top_lp.view(*lead, k) if k else None, top_ids.view(*lead, k) if k else None)
+    return Logprobs(None if y is None else f[4].view(lead), f[2].view(lead), f[3].view(lead),
+                    top_lp.view(*lead, k) if k else None, top_ids.view(*lead, k) if k else None,
+                    f[:2])
 
 
 def _row_grad(t: Optional[torch.Tensor], name: str, N: int, dev) -> Optional[torch.Tensor]:
@@ -88,8 +90,7 @@ def _row_grad(t: Optional[torch.Tensor], name: str, N: int, dev) -> Optional[tor
 
 
 def logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Tensor,
-                      lse: torch.Tensor, entropy: torch.Tensor,
-                      d_logprobs: Optional[torch.Tensor] = None,
+                      saved: torch.Tensor, d_logprobs: Optional[torch.Tensor] = None,
                       d_entropy: Optional[torch.Tensor] = None, ignore_index: int = -100,
                       softcap: float = 0.0, temperature: float = 1.0,
                       workspace: Optional[torch.Tensor] = None,
@@ -101,20 +102,18 @@ def logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.
                       check_status: bool = False
                       ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
     """dHidden [N, H] and dWeight [V, H] of sum(d_logprobs * logprobs + d_entropy *
-    entropy), either of them None for zeros.  lse and entropy are
-    logprobs_forward's; the gradient buffers and switches as for `backward`."""
+    entropy), either of them None for zeros.  `saved` is logprobs_forward's; the gradient buffers and switches as for `backward`."""
     if tokens is None:
         raise ValueError("the backward needs tokens (any valid ones if only d_entropy is given)")
-    if lse is None or (entropy is None and d_entropy is not None):
-        raise ValueError("the backward needs the forward's lse and, for d_entropy, its entropy")
     h2, w, y = _prep(hidden, weight, tokens)
     N, H = h2.shape
     V = w.shape[0]
     dev = h2.device
     a = _row_grad(d_logprobs, "d_logprobs", N, dev)
     b = _row_grad(d_entropy, "d_entropy", N, dev)
-    lse = _row_grad(lse, "lse", N, dev)
-    entropy = _row_grad(entropy, "entropy", N, dev)
+    if tuple(saved.shape) != (2, N) or saved.dtype != torch.float32 or saved.device != dev:
+        raise ValueError(f"saved must be logprobs_forward's float32 [2, {N}] tensor on {dev}")
+    saved = saved.contiguous()
     d_hidden, d_weight, flags = alloc_grads(N, H, V, dev, d_hidden, d_weight, accumulate_d_hidden,
                                             accumulate_d_weight, grad_dtype, compute_d_hidden,
                                             compute_d_weight)
@@ -124,7 +123,7 @@ def logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.
         check_workspace(workspace, dev)
     with on_device(dev):
         st = _lib().flce_logprobs_backward(
-            _ptr(h2), _ptr(w), _ptr(y), _ptr(lse), _ptr(entropy), N, H, V, int(ignore_index),
+            _ptr(h2), _ptr(w), _ptr(y), _ptr(saved), N, H, V, int(ignore_index),
             float(softcap), float(temperature), _DTYPES[h2.dtype], _ptr(a), _ptr(b),
             _ptr(d_hidden), _ptr(d_weight), flags, _ptr(workspace), workspace.numel(),
             _stream(dev))
@@ -138,31 +137,30 @@ class _LogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, tokens, ignore_index, softcap, temperature, top_k):
         out = logprobs_forward(hidden, weight, tokens, ignore_index, softcap, temperature, top_k)
-        ctx.save_for_backward(hidden, weight, tokens, out.lse, out.entropy)
+        ctx.save_for_backward(hidden, weight, tokens, out.saved)
         ctx.cfg = (ignore_index, softcap, temperature)
-        ctx.mark_non_differentiable(*(t for t in (out.lse, out.top_logprobs, out.top_ids)
-                                      if t is not None))
+        ctx.mark_non_differentiable(*(t for t in out[2:] if t is not None))
         ctx.set_materialize_grads(False)
         return tuple(out)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, d_logprobs, d_entropy, _d_lse, _d_top, _d_ids):
-        hidden, weight, tokens, lse, entropy = ctx.saved_tensors
+    def backward(ctx, d_logprobs, d_entropy, *_):
+        hidden, weight, tokens, saved = ctx.saved_tensors
         ignore_index, softcap, temperature = ctx.cfg
         need_dh, need_dw = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
         if not (need_dh or need_dw) or (d_logprobs is None and d_entropy is None):
             return (None,) * 7
         if tokens is None:  # only the entropy's gradient: any valid token will do
-            tokens = torch.zeros(lse.shape, dtype=torch.int64, device=lse.device)
+            tokens = torch.zeros(saved.shape[1], dtype=torch.int64, device=saved.device)
             ignore_index = -100
         # gradients in the parameters' own dtype (bf16 rounded once from fp32)
         dh = (torch.empty(hidden.shape, dtype=hidden.dtype, device=hidden.device)
               .view(-1, hidden.shape[-1]) if need_dh else None)
         dw = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device) \
             if need_dw else None
-        logprobs_backward(hidden, weight, tokens, lse, entropy, d_logprobs, d_entropy,
-                          ignore_index, softcap, temperature, d_hidden=dh, d_weight=dw,
+        logprobs_backward(hidden, weight, tokens, saved, d_logprobs, d_entropy, ignore_index,
+                          softcap, temperature, d_hidden=dh, d_weight=dw,
                           compute_d_hidden=need_dh, compute_d_weight=need_dw)
         return ((dh.view(hidden.shape) if need_dh else None), dw) + (None,) * 5
 
@@ -172,7 +170,7 @@ def fused_linear_logprobs(hidden: torch.Tensor, weight: torch.Tensor,
                           softcap: float = 0.0, temperature: float = 1.0,
                           top_k: int = 0) -> Logprobs:
     """Differentiable logprobs_forward: gradients of `logprobs` and `entropy` flow
-    to hidden and weight (policy-gradient losses, entropy bonuses); lse, top_logprobs and
-    top_ids carry none."""
+    to hidden and weight (policy-gradient losses, entropy bonuses); the other outputs
+    carry none."""
     return Logprobs(*_LogprobsFunction.apply(hidden, weight, tokens, ignore_index, softcap,
                                              temperature, top_k))

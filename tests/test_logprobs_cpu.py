@@ -76,12 +76,13 @@ def test_workspace_bytes(lib):
 
 
 def _fwd(lib, N=64, H=64, V=512, softcap=0.0, temperature=1.0, top_k=4, dtype=0, hidden=FAKE,
-         weight=FAKE, tokens=FAKE, logprobs=FAKE, entropy=FAKE, lse=FAKE, top=FAKE, ids=FAKE,
+         weight=FAKE, tokens=FAKE, logprobs=FAKE, entropy=FAKE, lse=FAKE, saved=FAKE, top=FAKE, ids=FAKE,
          ws=FAKE, ws_size=None):
     if ws_size is None:
         ws_size = lib.flce_logprobs_workspace_bytes(N, H, V, dtype, top_k) or 1 << 30
     return lib.flce_logprobs_forward(hidden, weight, tokens, N, H, V, -100, softcap, temperature,
-                                     top_k, dtype, logprobs, entropy, lse, top, ids, ws, ws_size,
+                                     top_k, dtype, logprobs, entropy, lse, saved, top, ids, ws,
+                                     ws_size,
                                      None)
 
 
@@ -98,7 +99,7 @@ def test_forward_refusals(lib):
     assert _fwd(lib, N=-1) == SHAPE
     assert _fwd(lib, V=0, top_k=0) == SHAPE
     assert _fwd(lib, H=12296, dtype=1) == SHAPE
-    for name in ("hidden", "weight", "entropy", "lse", "top", "ids", "ws"):
+    for name in ("hidden", "weight", "entropy", "lse", "saved", "top", "ids", "ws"):
         assert _fwd(lib, **{name: None}) == ARG, name
     # tokens and their log probabilities go together
     assert _fwd(lib, tokens=None) == ARG
@@ -110,22 +111,21 @@ def test_forward_refusals(lib):
     assert _fwd(lib, ws_size=256) == WS
 
 
-def _bwd(lib, N=64, H=64, V=512, temperature=1.0, entropy=FAKE, d_entropy=FAKE, d_hidden=FAKE,
-         d_weight=FAKE, flags=0, lse=FAKE, tokens=FAKE, ws_size=None):
+def _bwd(lib, N=64, H=64, V=512, temperature=1.0, d_hidden=FAKE, d_weight=FAKE, flags=0,
+         saved=FAKE, tokens=FAKE, ws_size=None):
     if ws_size is None:
         ws_size = lib.flce_workspace_bytes_ex(N, H, V, 0, 0)
-    return lib.flce_logprobs_backward(FAKE, FAKE, tokens, lse, entropy, N, H, V, -100, 0.0,
-                                      temperature, 0, FAKE, d_entropy, d_hidden, d_weight, flags,
-                                      FAKE, ws_size, None)
+    return lib.flce_logprobs_backward(FAKE, FAKE, tokens, saved, N, H, V, -100, 0.0, temperature,
+                                      0, FAKE, FAKE, d_hidden, d_weight, flags, FAKE, ws_size,
+                                      None)
 
 
 def test_backward_refusals(lib):
     assert _bwd(lib, temperature=0.0) == ARG
     assert _bwd(lib, temperature=float("nan")) == ARG
-    assert _bwd(lib, entropy=None) == ARG      # d_entropy needs the forward's entropy
     assert _bwd(lib, d_hidden=None, d_weight=None) == ARG
     assert _bwd(lib, flags=16) == ARG
-    assert _bwd(lib, lse=None) == ARG
+    assert _bwd(lib, saved=None) == ARG
     assert _bwd(lib, tokens=None) == ARG
     assert _bwd(lib, H=60) == SHAPE
     assert _bwd(lib, flags=8) == WS            # a bf16 dWeight needs the larger workspace
@@ -139,6 +139,6 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         flce.logprobs_forward(h, w)
     with pytest.raises(ValueError):
-        flce.logprobs_backward(h, w, y, torch.zeros(2), torch.zeros(2), torch.zeros(2))
+        flce.logprobs_backward(h, w, y, torch.zeros(2, 2), torch.zeros(2))
     with pytest.raises(ValueError):
         flce.fused_linear_logprobs(h.requires_grad_(), w, y)
