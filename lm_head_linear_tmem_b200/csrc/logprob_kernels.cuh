@@ -18,10 +18,8 @@ namespace flce {
 // kTopMargin more, because the lists are ordered by the tensor cores' fp32 logits
 // and the final order by the logits in fp64: an alternative is lost only if more
 // than kTopMargin others stand between its fp32 rank and top_k.
-// Every row keeps at least kMinTopList: see the correction in score_finish.
 constexpr int kMaxTopK = 32;
 constexpr int kTopMargin = 4;
-constexpr int kMinTopList = 8;
 constexpr int kMaxTopList = kMaxTopK + kTopMargin;
 
 // A running maximum that nothing has been merged into.  Finite, so that the
@@ -479,7 +477,7 @@ __global__ void __launch_bounds__(kScoreThreads)
 // with their fp64 values.  The backward recomputes the uncorrected logits: it gets
 // the uncorrected lse and entropy (`saved`), with which its 1 - p of a
 // dominant token keeps its leading digits.
-constexpr int kFinishThreads = 128;
+constexpr int kGroups = 128;  // of a row's lists, for the lower bound of the K-th best
 constexpr int kMaxHits = 512;
 constexpr int kMaxHitSlots = 256;
 
@@ -506,29 +504,36 @@ struct FinishArgs {
   unsigned int* status;
 };
 
+// This lane's part of a dot product, in four chains (a double addition's latency,
+// not its rate, is what a single one waits for).
 __device__ __forceinline__ double dot_part(const __nv_bfloat16* a, const __nv_bfloat16* b, int H,
                                            int lane) {
-  double acc = 0.0;
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
   for (int k = lane * 8; k < H; k += 256) {  // H is a multiple of 8
     const uint4 x = *reinterpret_cast<const uint4*>(a + k);
-    const uint4 y = *reinterpret_cast<const uint4*>(b + k);
+    const uint4 y = __ldg(reinterpret_cast<const uint4*>(b + k));
     const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x);
     const __nv_bfloat162* y2 = reinterpret_cast<const __nv_bfloat162*>(&y);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 u = __bfloat1622float2(x2[j]), v = __bfloat1622float2(y2[j]);
-      acc += static_cast<double>(u.x * v.x);
-      acc += static_cast<double>(u.y * v.y);
+      acc[j] += static_cast<double>(u.x * v.x);
+      acc[j] += static_cast<double>(u.y * v.y);
     }
   }
-  return acc;
+  return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
 __device__ __forceinline__ double dot_part(const float* a, const float* b, int H, int lane) {
-  double acc = 0.0;
-  for (int k = lane; k < H; k += 32)
-    acc = fma(static_cast<double>(a[k]), static_cast<double>(b[k]), acc);
-  return acc;
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  int k = lane;
+  for (; k + 96 < H; k += 128)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc[j] = fma(static_cast<double>(a[k + 32 * j]), static_cast<double>(b[k + 32 * j]), acc[j]);
+  for (; k < H; k += 32) acc[0] = fma(static_cast<double>(a[k]), static_cast<double>(b[k]), acc[0]);
+  return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
 // The softcap as the partial results have it.
@@ -543,7 +548,9 @@ __device__ __forceinline__ float gemm_softcap<float>(float z, float softcap) {
   return capped(z, softcap);
 }
 
-template <class T>
+// kFinishThreads: 128, or 512 where there are so few rows that one row's latency
+// (its K + 1 dot products above all) is the kernel's time.
+template <class T, int kFinishThreads>
 __global__ void __launch_bounds__(kFinishThreads)
     score_finish_kernel(const T* __restrict__ hidden, const T* __restrict__ weight,
                         const FinishArgs a) {
@@ -555,8 +562,9 @@ __global__ void __launch_bounds__(kFinishThreads)
   __shared__ TopEntry hits[kMaxHits], wbest[2][kWarps];
   __shared__ int ids[kMaxTopList + 1];
   __shared__ float za[kMaxTopList];
-  __shared__ double zx[kMaxTopList + 1];
+  __shared__ double zx[kMaxTopList + 1], xe[kMaxTopList + 1];
   __shared__ double lse_sh;
+  static_assert(kFinishThreads % kGroups == 0 && kMaxTopList < kGroups, "groups of lists");
   griddep_wait();
   const int j = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int row = a.perm != nullptr ? a.perm[j] : j;
@@ -601,7 +609,7 @@ __global__ void __launch_bounds__(kFinishThreads)
                           __shfl_down_sync(0xffffffffu, st.t, o)});
   if (lane == 0) wst[warp] = st;
 
-  // ---- the K best entries.  The K-th largest of the threads' maxima is a lower
+  // ---- the K best entries.  The K-th largest of the groups' maxima is a lower
   // bound of the K-th best (each is an entry of its own), and about K lists have
   // entries that reach it.  Those entries are ranked against one another; if
   // ties make them more than fit, the K best are taken one by one from all lists.
@@ -612,14 +620,23 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   if (t <= a.K) ids[t] = -1;
   __syncthreads();
-  {
-    int above = 0, ties = 0;
-#pragma unroll 8
-    for (int i = 0; i < kFinishThreads; ++i) {
-      above += tmaxs[i] > tmax ? 1 : 0;
-      ties += tmaxs[i] == tmax ? 1 : 0;
+  float gmax = tmax;
+  if constexpr (kFinishThreads > kGroups) {  // a group's maximum, over its threads
+    if (t < kGroups) {
+#pragma unroll
+      for (int i = kGroups; i < kFinishThreads; i += kGroups) gmax = fmaxf(gmax, tmaxs[t + i]);
+      tmaxs[t] = gmax;
     }
-    if (above < a.K && above + ties >= a.K) bound_sh = tmax;  // one value whoever writes it
+    __syncthreads();
+  }
+  if (t < kGroups) {
+    int above = 0, ties = 0;
+#pragma unroll 16
+    for (int i = 0; i < kGroups; ++i) {
+      above += tmaxs[i] > gmax ? 1 : 0;
+      ties += tmaxs[i] == gmax ? 1 : 0;
+    }
+    if (above < a.K && above + ties >= a.K) bound_sh = gmax;  // one value whoever writes it
   }
   __syncthreads();
   const float bound = bound_sh;
@@ -699,68 +716,67 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   __syncthreads();
 
-  // ---- outputs
+  // ---- outputs.  xe: the listed logits as the softmax sees them
   const double ln2 = 0.693147180559945309417;
-  auto capped64 = [&](double z) { return a.softcap > 0.f ? a.softcap * tanh(z / a.softcap) : z; };
+  double x = 0.0;
+  if (t <= a.K) {
+    const double z = zx[t];
+    x = (a.softcap > 0.f ? a.softcap * tanh(z / a.softcap) : z) * a.inv_temp;
+    xe[t] = x;
+  }
+  __syncthreads();
   if (warp == 0) {
     st = wst[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) stats_merge(st, wst[w]);
-    auto sum = [](double v) {
+    auto sum = [](float v) {
 #pragma unroll
       for (int o = 16; o >= 1; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
       return v;
     };
-    // log2-domain values of the listed logits, from the GEMM (xa) and in fp64 (xe)
-    const double to_log2 = a.inv_temp / ln2;
-    const double M = st.m, Me = M * a.nat / ln2;  // in the fp32 scale's units; exactly
-    double s_rest = 0.0, t_rest = 0.0, m1 = Me;
+    const double Me = static_cast<double>(st.m) * a.nat;  // the GEMM's maximum
+    double m1 = Me;
+    float s_rest = 0.f, t_rest = 0.f;
     for (int c = lane; c < a.K; c += 32) {
       if (ids[c] < 0) continue;
       const float L = a.softcap > 0.f ? gemm_softcap<T>(za[c], a.softcap) : za[c];
-      const double da = fmax(static_cast<double>(L) * a.scale - M, double(kLowExp2));
-      const double e = exp2(da);
+      const float d = fmaxf(fmaf(L, a.scale, -st.m), kLowExp2);
+      const float e = exp2f(d);
       s_rest += e;
-      t_rest += e * da;
-      m1 = fmax(m1, capped64(zx[c]) * to_log2);
+      t_rest = fmaf(e, d, t_rest);
+      m1 = fmax(m1, xe[c]);
     }
-    s_rest = sum(s_rest);
-    t_rest = sum(t_rest);
+    // what the listed ones leave (a NaN sum stays NaN)
+    s_rest = st.s - sum(s_rest);
+    t_rest = st.t - sum(t_rest);
+    if (s_rest < 0.f) s_rest = 0.f;
+    if (t_rest > 0.f) t_rest = 0.f;
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-    // what the listed ones leave (a NaN sum stays NaN), at the new maximum
-    s_rest = st.s - s_rest;
-    t_rest = st.t - t_rest;
-    if (s_rest < 0.0) s_rest = 0.0;
-    if (t_rest > 0.0) t_rest = 0.0;
-    const double down = exp2(Me - m1);
-    double s1 = 0.0, t1 = 0.0;
+    // ... and with their fp64 values, at the largest of those
+    float s1 = 0.f, t1 = 0.f;
     for (int c = lane; c < a.K; c += 32) {
       if (ids[c] < 0) continue;
-      const double de = fmax(capped64(zx[c]) * to_log2 - m1, double(kLowExp2));
-      const double e = exp2(de);
+      const float d = fmaxf(static_cast<float>((xe[c] - m1) / ln2), kLowExp2);
+      const float e = exp2f(d);
       s1 += e;
-      t1 += e * de;
+      t1 = fmaf(e, d, t1);
     }
+    const float shift = static_cast<float>((Me - m1) / ln2), down = exp2f(shift);
     s1 = sum(s1) + s_rest * down;
-    t1 = sum(t1) + (t_rest + s_rest * (Me - m1)) * down;
+    t1 = sum(t1) + (s_rest == 0.f ? t_rest : fmaf(s_rest, shift, t_rest)) * down;
     if (lane == 0) {
-      const double log2_s = s1 == 0.0 ? -CUDART_INF : log2(s1);
-      const double lse = ln2 * (m1 + log2_s);
+      const float log2_s = log2f(s1), log2_a = log2f(st.s);  // of 0: -inf
+      const double lse = m1 + ln2 * log2_s;
       lse_sh = lse;
       a.lse[row] = static_cast<float>(lse);
-      a.entropy[row] = static_cast<float>(ln2 * (log2_s - t1 / s1));
-      const double log2_a = st.s == 0.f ? -CUDART_INF : log2(static_cast<double>(st.s));
-      a.saved[row] = static_cast<float>(M * a.nat + ln2 * log2_a);
-      a.saved[a.N + row] = static_cast<float>(ln2 * (log2_a - static_cast<double>(st.t) / st.s));
+      a.entropy[row] = static_cast<float>(ln2) * (log2_s - t1 / s1);
+      a.saved[row] = static_cast<float>(Me + ln2 * log2_a);
+      a.saved[a.N + row] = static_cast<float>(ln2) * (log2_a - st.t / st.s);
     }
   }
   __syncthreads();
-  const double lse = lse_sh;
-  auto logprob = [&](double z) -> float {
-    return static_cast<float>(capped64(z) * a.inv_temp - lse);
-  };
-  if (t == 32 && a.logprobs != nullptr) a.logprobs[row] = logprob(zx[a.K]);
+  if (t == a.K && a.logprobs != nullptr) a.logprobs[row] = static_cast<float>(x - lse_sh);
   if (t < a.K) {
     const int id = ids[t];
     auto ordered = [](double z) { return z != z ? -CUDART_INF : z; };  // NaN (inf - inf) last
@@ -776,7 +792,8 @@ __global__ void __launch_bounds__(kFinishThreads)
         rank += (ic >= 0 && (zc > z || (zc == z && ic < id))) ? 1 : 0;
     }
     if (rank < a.top_k) {
-      a.top_logprobs[static_cast<size_t>(row) * a.top_k + rank] = logprob(zx[t]);
+      a.top_logprobs[static_cast<size_t>(row) * a.top_k + rank] =
+          static_cast<float>(x - lse_sh);
       a.top_ids[static_cast<size_t>(row) * a.top_k + rank] = id;
     }
   }

@@ -30,7 +30,7 @@ struct ScorePlan {
 
 ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k) {
   ScorePlan P{};
-  P.K = static_cast<int>(std::min<int64_t>(std::max(top_k + kTopMargin, kMinTopList), V));
+  P.K = static_cast<int>(std::min<int64_t>(top_k + kTopMargin, V));
   if (!bf16) {
     P.slots = static_cast<int>((V + kScoreCols - 1) / kScoreCols);
     return P;
@@ -112,12 +112,16 @@ flce_status check_score(const Opts& o, const void* hidden, const void* weight, i
   return FLCE_OK;
 }
 
-template <class T>
-cudaError_t run_finish(const void* hidden, const void* weight, const FinishArgs& a,
+// Rows up to which score_finish gives each row a block of 512 threads (two for
+// every SM) instead of 128.
+constexpr int kFinishFewRows = 2 * kPlanSms;
+
+template <class T, int kThreads>
+cudaError_t run_finish_with(const void* hidden, const void* weight, const FinishArgs& a,
                        cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.N), 1, 1);
-  cfg.blockDim = dim3(kFinishThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -126,10 +130,17 @@ cudaError_t run_finish(const void* hidden, const void* weight, const FinishArgs&
   cfg.numAttrs = 1;
   cudaError_t le = cudaSuccess;
   const cudaError_t e = launch(kFwdMerge, st, [&] {
-    le = cudaLaunchKernelEx(&cfg, score_finish_kernel<T>, static_cast<const T*>(hidden),
+    le = cudaLaunchKernelEx(&cfg, score_finish_kernel<T, kThreads>, static_cast<const T*>(hidden),
                             static_cast<const T*>(weight), a);
   });
   return le != cudaSuccess ? le : e;
+}
+
+template <class T>
+cudaError_t run_finish(const void* hidden, const void* weight, const FinishArgs& a,
+                       cudaStream_t st) {
+  return a.N <= kFinishFewRows ? run_finish_with<T, 512>(hidden, weight, a, st)
+                               : run_finish_with<T, 128>(hidden, weight, a, st);
 }
 
 flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout& L,

@@ -49,7 +49,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle alone: making a torch.cuda.Stream of it costs 2 us a call
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def on_device(device: torch.device):
