@@ -78,26 +78,30 @@ __device__ __forceinline__ bool better(TopEntry a, TopEntry b) {
 // ------------------------------------------------------------------ GEMM epilogue
 // A CTA works on runs of consecutive column tiles of one row tile, so a thread
 // sees one row's logits over a long range of columns and keeps that row's state
-// in registers (statistics) and shared memory (list) until the run ends:
-// partial results per row and run instead of per row and tile, and a list that
-// soon turns nearly every column down with one comparison of the maximum of 32.
-// `seen` holds, for each row, the maxima of K groups of the columns that any CTA
-// has seen (32-column chunks, dealt out in turn): the least of them is a lower
-// bound of the row's K-th best.  With it the lists of later runs start where the
-// earlier ones have got to: about ln(K + 1) K / n of the columns are candidates
-// after n columns.  A logit below the bound cannot be among the K best; equal ones
-// are kept, because a lower id wins.  The K best by (logit, lowest id) are in the
-// lists whatever the order in which runs are worked on, so the results do not
-// depend on it.
-// kCap: entries a list has room for.  16 fit beside the four-stage operand ring
-// of the other epilogues; kMaxTopList leave three stages.
-constexpr int kSmallTopList = 16;
+// in registers until the run ends: partial results per row and run instead of
+// per row and tile.  Candidates for the row's K best are appended to the run's list
+// in global memory by stores that nothing waits for.  (The tensor cores and TMA
+// keep shared memory and the L1 busy: lists there, or in local memory, cost 1000 to
+// 13000 clocks an update, against the 33000 clocks that a 256 x 512 tile's MMAs
+// take at H = 2048.)
+// What keeps candidates few: `seen` holds, for each row, the maxima of K groups of
+// the columns that any CTA has seen (128-column blocks, dealt out in turn); the
+// least of them is a lower bound of the row's K-th best.  A logit below it cannot
+// be among the K best; equal ones are kept, because a lower id wins.  About
+// ln(K + 1) K / n of the columns are candidates after n columns.
+// The K best by (logit, lowest id) are in the lists whatever the order in which
+// runs are worked on, so the results do not depend on it.
 
-template <bool kSoftcap, int kCap>
+// Entries of a run's list: room for the K best and K new ones (see scan), and some
+// more so that this limit seldom counts.
+constexpr int top_list_cap(int K) { return 2 * K + 8; }
+constexpr int kMaxTopCap = top_list_cap(kMaxTopList);
+
+template <bool kSoftcap>
 struct ScoreEpi {
   static constexpr bool kRun = true;
   static constexpr int kEpiWarps = 8;
-  static constexpr int kStagingPerWarp = 32 * kCap * 8;  // [kCap][32] values, then ids
+  static constexpr int kStagingPerWarp = 32 * 32 * 4;  // 32 columns of 32 rows (see scan)
   __device__ static void init_smem(uint8_t*) {}
 
   struct Params {
@@ -109,22 +113,18 @@ struct ScoreEpi {
     RunMap map;
     int tile_cols;
     int slots;        // 2 * runs per row (the two warps of a row, half a bank each)
-    int K;            // list length, at most kCap
-    float4* part;     // [N][slots]: m, s, t, largest entry of the list (-inf: none)
+    int K;
+    float4* part;     // [N][slots]: m, s, t, largest logit of the run (-inf: none)
     int* count;       // [N][slots]: entries of the list
-    TopEntry* lists;  // [N][slots][K], in no order
+    TopEntry* lists;  // [N][slots][top_list_cap(K)], ids ascending
     uint32_t* seen;   // [K][N] order_key of the groups' maxima; zeroed before the launch
   };
 
-  // The list is not sorted: a candidate takes the place of the worst entry (-inf
-  // while there is room), and one pass over the values, whose loads do not wait
-  // for one another, finds the next worst.  All lanes go through that together:
-  // left to diverge, the lanes' passes ran one after another, 13000 clocks for
-  // 32 columns.
   struct State {
     Stats st;
-    float kth;    // value of the worst entry
-    int worst;    // place of the worst entry
+    float zmax;   // largest logit of the run
+    float above;  // candidates are larger than this
+    int n;        // entries of the list
   };
 
   struct Pre {
@@ -140,103 +140,165 @@ struct ScoreEpi {
     return Pre{order_value(least)};
   }
 
-  // This lane's list: entry i at lv[32 * i], li[32 * i].
-  struct List {
-    float* lv;
-    int* li;
-  };
-
-  // The lanes with `take` (v > S.kth) put an entry into their lists.  Ids come in
-  // ascending order, so of equal values the one with the highest id is the worst
-  // and a newcomer equal to the worst stays out.
-  __device__ static void put(State& S, List L, int K, bool take, float v, int id) {
-    if (take) {
-      L.lv[32 * S.worst] = v;
-      L.li[32 * S.worst] = id;
-    }
-    __syncwarp();
-    float mv = CUDART_INF_F;
-    int at = 0;
-    bool equal = false;
-#pragma unroll 4
-    for (int i = 0; i < K; ++i) {
-      const float x = L.lv[32 * i];
-      equal = x == mv || (equal && x >= mv);
-      at = x < mv ? i : at;
-      mv = fminf(mv, x);
-    }
-    equal = take && equal && mv > -CUDART_INF_F;
-    if (__any_sync(0xffffffffu, equal)) {
-      for (int i = 0; i < K; ++i)
-        if (L.lv[32 * i] == mv && L.li[32 * i] > L.li[32 * at]) at = equal ? i : at;
-      __syncwarp();
-    }
-    S.kth = take ? mv : S.kth;
-    S.worst = take ? at : S.worst;
-  }
-
-  // r[j] of a lane's own j, by halving: local memory (what an indexed array would
-  // become) has no room in the L1 beside the operand ring and took 3000 clocks a
-  // chunk and more.
-  __device__ static float pick(const uint32_t (&r)[32], int j) {
-    uint32_t x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = (j & 16) ? r[i + 16] : r[i];
-#pragma unroll
-    for (int w = 8; w >= 1; w /= 2)
-#pragma unroll
-      for (int i = 0; i < w; ++i) x[i] = (j & w) ? x[i + w] : x[i];
-    return __uint_as_float(x[0]);
-  }
-
-  // The candidates among 32 columns starting at `col`: those above the list's
-  // worst and `bound` (exclusive); mx is the columns' maximum.  Each round every
-  // lane takes its next one.
-  __device__ static void scan32(State& S, List L, int K, float bound, const uint32_t (&r)[32],
-                                float mx, int col) {
-    const float b = fmaxf(S.kth, bound);
-    if (!__any_sync(0xffffffffu, mx > b)) return;
-    // v > b is the sign of b - v (a NaN has none): no predicates to wait for
+  // Bit j: r[j] > b, by the sign of b - r[j] (a NaN has none): no predicates to wait for.
+  __device__ static uint32_t larger(const uint32_t (&r)[32], float b) {
     uint32_t h[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 7; j >= 0; --j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         h[i] = __funnelshift_l(__float_as_uint(b - __uint_as_float(r[8 * i + j])), h[i], 1);
-    uint32_t hits = h[0] | h[1] << 8 | h[2] << 16 | h[3] << 24;
-    while (__any_sync(0xffffffffu, hits != 0u)) {
-      const int j = hits != 0u ? __ffs(hits) - 1 : 0;
-      const float v = pick(r, j);
-      const bool take = hits != 0u && v > S.kth;
-      hits &= hits - 1u;
-      if (__any_sync(0xffffffffu, take)) put(S, L, K, take, v, col + j);
-    }
+    return h[0] | h[1] << 8 | h[2] << 16 | h[3] << 24;
   }
 
-  // A lower bound of the K-th best of 128 columns (-inf if there are too few), by
-  // bisection between the least and the largest.  Without it the first columns
-  // of a run, which find no bound, would nearly all go through put().
-  __device__ static float first_bound(const uint32_t (&r)[4][32], int K, float mx) {
-    float lo = mx;
+  // How many of n values are at least x (a NaN counts as large: the alternatives
+  // of such a row are not defined).
+  template <int n, class F>
+  __device__ static int at_least(const F& value, float x) {
+    uint32_t below[4] = {0u, 0u, 0u, 0u};  // v < x is the sign of v - x
 #pragma unroll
-    for (int j = 0; j < 128; ++j) {
-      const float v = __uint_as_float(r[j / 32][j % 32]);
-      lo = fminf(lo, v == -CUDART_INF_F ? mx : v);
+    for (int j = 0; j < n; ++j) below[j & 3] += __float_as_uint(value(j) - x) >> 31;
+    return n - static_cast<int>((below[0] + below[1]) + (below[2] + below[3]));
+  }
+
+  // The K-th largest of n values none of which exceeds mx (-inf if there are fewer).
+  template <int n, class F>
+  __device__ static float kth_largest(const F& value, int K, float mx) {
+    uint32_t lo = order_key(-CUDART_INF_F), hi = order_key(mx);
+    while (__any_sync(0xffffffffu, lo < hi)) {
+      const uint32_t mid = lo + (hi - lo + 1u) / 2u;
+      if (at_least<n>(value, order_value(mid)) >= K)
+        lo = mid;
+      else
+        hi = mid > lo ? mid - 1u : lo;
     }
-    float hi = mx, x = lo, bound = -CUDART_INF_F;
+    return order_value(lo);
+  }
+
+  // A lower bound of the K-th largest of 128 columns (-inf if it finds none) that
+  // not many more than K reach.  It starts from the least of the four chunks'
+  // maxima, which about nine columns reach, goes down in growing steps while
+  // fewer than K reach it, and then halves; the second largest maximum is the
+  // upper end, so that one logit far above the others does not stretch the range.
+  __device__ static float near_kth(const uint32_t (&r)[4][32], int K, const float (&mx)[4]) {
+    const auto value = [&](int j) { return __uint_as_float(r[j / 32][j % 32]); };
+    const float a0 = fminf(mx[0], mx[1]), a1 = fmaxf(mx[0], mx[1]);
+    const float b0 = fminf(mx[2], mx[3]), b1 = fmaxf(mx[2], mx[3]);
+    float hi = fmaxf(fminf(a1, b1), fmaxf(a0, b0)), x = fminf(a0, b0);
+    float step = hi - x, bound = -CUDART_INF_F;
 #pragma unroll 1
-    for (int it = 0; it < 6; ++it) {
-      uint32_t below[4] = {0u, 0u, 0u, 0u};  // v < x is the sign of v - x
-#pragma unroll
-      for (int j = 0; j < 128; ++j)
-        below[j & 3] += __float_as_uint(__uint_as_float(r[j / 32][j % 32]) - x) >> 31;
-      if (128 - static_cast<int>((below[0] + below[1]) + (below[2] + below[3])) >= K)
-        bound = lo = x;
+    for (int it = 0; it < 8; ++it) {
+      const int n = at_least<128>(value, x);
+      if (n >= K)
+        bound = x;
       else
         hi = x;
-      x = 0.5f * lo + 0.5f * hi;
+      // (NaN bounds, from infinities, end the search where it is)
+      const bool done = (n >= K && n <= K + K / 2 + 2) || !(hi > bound);
+      if (__all_sync(0xffffffffu, done)) break;
+      if (!done) {
+        x = bound > -CUDART_INF_F ? 0.5f * bound + 0.5f * hi : x - step;
+        step *= 2.f;
+      }
     }
     return bound;
+  }
+
+  // Appends the candidates among the 128 columns starting at `col`; mx are the
+  // maxima of 32 columns each.  Most often no lane has more than one, which then is
+  // its maximum.  Where a list has no room for all of a lane's candidates, the
+  // block's own K best will do (there is room for K: tidy() sees to it).
+  __device__ static void scan(State& S, TopEntry* list, int K, const uint32_t (&r)[4][32],
+                              const float (&mx)[4], float mx_all, int col, float* stage) {
+    if (!__any_sync(0xffffffffu, mx_all > S.above)) return;
+    uint32_t hits[4];
+    const auto find = [&](float above) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        hits[c] = __any_sync(0xffffffffu, mx[c] > above) ? larger(r[c], above) : 0u;
+      return (__popc(hits[0]) + __popc(hits[1])) + (__popc(hits[2]) + __popc(hits[3]));
+    };
+    int n = find(S.above);
+    float kth = -CUDART_INF_F;
+    if (__any_sync(0xffffffffu, n > K + 8)) {
+      // a run's start, before any CTA has seen enough of the row (or logits that
+      // rise with the id): all but the block's own best would be for nothing
+      kth = near_kth(r, K, mx);
+      n = find(fmaxf(S.above, nextbelow(kth)));
+    }
+    const bool full = n > top_list_cap(K) - S.n;
+    if (__any_sync(0xffffffffu, full)) {
+      const float x = kth_largest<128>(
+          [&](int j) { return __uint_as_float(r[j / 32][j % 32]); }, K, mx_all);
+      // those above x, and of those equal to x the first ones up to K
+      uint32_t gt[4], eq[4];
+      int room = K;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        gt[c] = larger(r[c], x);
+        eq[c] = larger(r[c], nextbelow(x)) & ~gt[c];
+        room -= __popc(gt[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        while (__popc(eq[c]) > max(room, 0)) eq[c] &= ~(0x80000000u >> __clz(eq[c]));
+        room -= __popc(eq[c]);
+        if (full) hits[c] = gt[c] | eq[c];
+      }
+      if (full) {
+        n = __popc(hits[0]) + __popc(hits[1]) + __popc(hits[2]) + __popc(hits[3]);
+        S.above = fmaxf(S.above, x);
+      }
+    }
+    if (!__any_sync(0xffffffffu, n > 1)) {
+      int j = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (hits[c] != 0u) j = c * 32 + __ffs(hits[c]) - 1;
+      if (n > 0) list[S.n++] = TopEntry{mx_all, col + j};
+    } else {
+      // through shared memory, where a lane can take column j of its own: a short
+      // loop, for code that is seldom run waits for its instructions (32 unrolled
+      // conditional stores took 10000 clocks)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!__any_sync(0xffffffffu, hits[c] != 0u)) continue;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) stage[32 * j] = __uint_as_float(r[c][j]);
+        __syncwarp();
+        for (uint32_t h = hits[c]; h != 0u; h &= h - 1u) {
+          const int j = __ffs(h) - 1;
+          list[S.n++] = TopEntry{stage[32 * j], col + c * 32 + j};
+        }
+      }
+    }
+    S.above = fmaxf(S.above, kth);  // K columns with lower ids reach kth
+  }
+
+  // Cuts a list that may have no room for K more down to its own K best.
+  __device__ static void tidy(State& S, TopEntry* list, int K) {
+    const bool full = S.n > top_list_cap(K) - K;
+    if (!__any_sync(0xffffffffu, full)) return;
+    float e[kMaxTopCap];
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < kMaxTopCap; ++i) {
+      e[i] = i < S.n ? list[i].v : -CUDART_INF_F;
+      top = fmaxf(top, e[i]);
+    }
+    const float x = kth_largest<kMaxTopCap>([&](int i) { return e[i]; }, K, top);
+    if (!full) return;
+    int room = K;
+#pragma unroll
+    for (int i = 0; i < kMaxTopCap; ++i) room -= e[i] > x ? 1 : 0;
+    int n = 0;
+    for (int i = 0; i < S.n; ++i) {
+      const TopEntry c = list[i];
+      if (c.v > x || (c.v == x && room-- > 0)) list[n++] = c;
+    }
+    S.n = n;
+    S.above = fmaxf(S.above, x);  // later ids that equal x come after K others
   }
 
   __device__ static float max32(const uint32_t (&r)[32]) {
@@ -260,18 +322,18 @@ struct ScoreEpi {
     }
     const int row = m_base + q * 32 + lane;
     const bool row_ok = row < p.N;
-    const List L{reinterpret_cast<float*>(stg) + lane,
-                 reinterpret_cast<int*>(stg) + 32 * kCap + lane};
     const int run = p.map.of_tile(col0 / p.tile_cols);
     int run_start, run_len;
     p.map.of_run(run, run_start, run_len);
     const bool first = col0 == run_start * p.tile_cols;
     if (first) {
       S.st = Stats{kNoMax, 0.f, 0.f};
-      S.kth = row_ok ? -CUDART_INF_F : CUDART_INF_F;  // rows past the end take nothing
-      S.worst = 0;
-      for (int i = 0; i < p.K; ++i) L.lv[32 * i] = -CUDART_INF_F;
+      S.zmax = -CUDART_INF_F;
+      S.above = row_ok ? -CUDART_INF_F : CUDART_INF_F;  // rows past the end take nothing
+      S.n = 0;
     }
+    const size_t at = static_cast<size_t>(row) * p.slots + run * 2 + part;
+    TopEntry* list = p.lists + at * top_list_cap(p.K);
     const int h0 = col0 + part * (BN / 2);  // this warp's first column
     const int ncols = max(0, min(BN / 2, p.V - h0));
     const uint32_t ta = taddr + part * (BN / 2);
@@ -294,26 +356,24 @@ struct ScoreEpi {
     float mx_all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 
     // ---- list
-    // (the largest float below the rows' bound: an equal logit may still count)
-    float bound = pre.bound;
-    if (first && __any_sync(0xffffffffu, bound == -CUDART_INF_F))
-      bound = fmaxf(bound, first_bound(r, p.K, mx_all));
-    bound = nextbelow(bound);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) scan32(S, L, p.K, bound, r[c], mx[c], h0 + c * 32);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (row_ok && mx[c] > pre.bound)
-        atomicMax(p.seen + static_cast<size_t>((h0 / 32 + c) % p.K) * p.N + row,
-                  order_key(mx[c]));
+    S.zmax = fmaxf(S.zmax, mx_all);
+    S.above = fmaxf(S.above, nextbelow(pre.bound));  // (an equal logit may still count)
+    scan(S, list, p.K, r, mx, mx_all, h0, reinterpret_cast<float*>(stg) + lane);
+    if (row_ok && mx_all > pre.bound)
+      atomicMax(p.seen + static_cast<size_t>(h0 / (BN / 2) % p.K) * p.N + row,
+                order_key(mx_all));
 
     // ---- statistics
     if constexpr (kSoftcap) {
       auto cap = [&](float z) { return p.softcap * tanh_exp2(z * p.inv_softcap); };
 #pragma unroll
       for (int j = 0; j < 128; ++j)
-        r[j / 32][j % 32] = __float_as_uint(
-            j < ncols ? cap(__uint_as_float(r[j / 32][j % 32])) : -CUDART_INF_F);
+        r[j / 32][j % 32] = __float_as_uint(cap(__uint_as_float(r[j / 32][j % 32])));
+      if (ncols < BN / 2) {  // the cap has made columns past the end -softcap
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+          if (j >= ncols) r[j / 32][j % 32] = __float_as_uint(-CUDART_INF_F);
+      }
       // the cap keeps the order: the capped maximum is the maximum's cap (-inf: no columns)
       mx_all = ncols > 0 ? cap(mx_all) : -CUDART_INF_F;
     }
@@ -332,19 +392,11 @@ struct ScoreEpi {
     st.t += (t4[0] + t4[1]) + (t4[2] + t4[3]);
 
     const int run_end = min((run_start + run_len) * p.tile_cols, (p.V + BN - 1) / BN * BN);
-    if (col0 + BN >= run_end && row_ok) {  // the run's last bank
-      const size_t at = static_cast<size_t>(row) * p.slots + run * 2 + part;
-      TopEntry* o = p.lists + at * p.K;
-      float best = -CUDART_INF_F;
-      int n = 0;
-      for (int i = 0; i < p.K; ++i) {
-        const TopEntry x{L.lv[32 * i], L.li[32 * i]};
-        if (x.v == -CUDART_INF_F) break;  // places are filled in order
-        best = fmaxf(best, x.v);
-        o[n++] = x;
-      }
-      p.part[at] = make_float4(st.m, st.s, st.t, best);
-      p.count[at] = n;
+    if (col0 + BN < run_end) {
+      tidy(S, list, p.K);
+    } else if (row_ok) {  // the run's last bank
+      p.part[at] = make_float4(st.m, st.s, st.t, S.zmax);
+      p.count[at] = S.n;
     }
     return true;
   }
@@ -361,7 +413,7 @@ constexpr int kScoreThreads = 256;
 template <int kRows>
 __global__ void __launch_bounds__(kScoreThreads)
     score_simt_kernel(const float* __restrict__ hidden, const float* __restrict__ weight, int N,
-                      int H, int V, float softcap, float scale, int slots, int K,
+                      int H, int V, float softcap, float scale, int slots, int K, int cap,
                       float4* __restrict__ part, int* __restrict__ count,
                       TopEntry* __restrict__ lists) {
   extern __shared__ float sh[];
@@ -447,7 +499,7 @@ __global__ void __launch_bounds__(kScoreThreads)
       if (id < 0) break;
       top = fmaxf(top, best);
       if (lane == 0) {
-        lists[at * K + n] = TopEntry{best, v0 + id};
+        lists[at * cap + n] = TopEntry{best, v0 + id};
         z[id] = -CUDART_INF_F;
       }
       __syncwarp();
@@ -491,7 +543,7 @@ struct FinishArgs {
   double inv_temp;   // 1 / temperature
   double nat;        // 1 / (temperature * scale)
   float scale;       // log2(e) / temperature in fp32, as the partial results have it
-  int slots, K, top_k;
+  int slots, K, cap, top_k;  // cap: entries between one list's start and the next's
   const float4* part;
   const int* count;
   const TopEntry* lists;
@@ -591,10 +643,10 @@ __global__ void __launch_bounds__(kFinishThreads)
     return;
   }
 
-  // ---- statistics, and the largest entry of this thread's lists
+  // ---- statistics, and the largest logit of this thread's slots
   const float4* part = a.part + static_cast<size_t>(j) * a.slots;
   const int* count = a.count + static_cast<size_t>(j) * a.slots;
-  const TopEntry* lists = a.lists + static_cast<size_t>(j) * a.slots * a.K;
+  const TopEntry* lists = a.lists + static_cast<size_t>(j) * a.slots * a.cap;
   Stats st{kNoMax, 0.f, 0.f};
   float tmax = -CUDART_INF_F;
   for (int i = t; i < a.slots; i += kFinishThreads) {
@@ -610,7 +662,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (lane == 0) wst[warp] = st;
 
   // ---- the K best entries.  The K-th largest of the groups' maxima is a lower
-  // bound of the K-th best (each is an entry of its own), and about K lists have
+  // bound of the K-th best (each is a logit of its own), and about K lists have
   // entries that reach it.  Those entries are ranked against one another; if
   // ties make them more than fit, the K best are taken one by one from all lists.
   tmaxs[t] = tmax;
@@ -648,11 +700,11 @@ __global__ void __launch_bounds__(kFinishThreads)
       }
   __syncthreads();
   if (n_hit_slots <= kMaxHitSlots) {
-    for (int e = t; e < n_hit_slots * a.K; e += kFinishThreads) {
-      const int h = e / a.K, i = e - h * a.K;
+    for (int e = t; e < n_hit_slots * a.cap; e += kFinishThreads) {
+      const int h = e / a.cap, i = e - h * a.cap;
       const int l = hit_slots[h] & 0xffffff;
       if (i >= hit_slots[h] >> 24) continue;
-      const TopEntry x = lists[static_cast<size_t>(l) * a.K + i];
+      const TopEntry x = lists[static_cast<size_t>(l) * a.cap + i];
       if (x.v >= bound) {
         const int at = atomicAdd(&n_hits, 1);
         if (at < kMaxHits) hits[at] = x;
@@ -675,7 +727,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     for (int n = 0; n < a.K; ++n) {
       TopEntry best{-CUDART_INF_F, -1};
       for (int l = t; l < a.slots; l += kFinishThreads) {
-        const TopEntry* e = lists + static_cast<size_t>(l) * a.K;
+        const TopEntry* e = lists + static_cast<size_t>(l) * a.cap;
         for (int i = 0; i < count[l]; ++i) {
           const TopEntry x = e[i];
           if (better(last, x) && (best.id < 0 || better(x, best))) best = x;
@@ -717,7 +769,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   __syncthreads();
 
   // ---- outputs.  xe: the listed logits as the softmax sees them
-  const double ln2 = 0.693147180559945309417;
+  const double ln2 = 0.693147180559945309417, log2e = 1.442695040888963407360;
   double x = 0.0;
   if (t <= a.K) {
     const double z = zx[t];
@@ -757,12 +809,12 @@ __global__ void __launch_bounds__(kFinishThreads)
     float s1 = 0.f, t1 = 0.f;
     for (int c = lane; c < a.K; c += 32) {
       if (ids[c] < 0) continue;
-      const float d = fmaxf(static_cast<float>((xe[c] - m1) / ln2), kLowExp2);
+      const float d = fmaxf(static_cast<float>((xe[c] - m1) * log2e), kLowExp2);
       const float e = exp2f(d);
       s1 += e;
       t1 = fmaf(e, d, t1);
     }
-    const float shift = static_cast<float>((Me - m1) / ln2), down = exp2f(shift);
+    const float shift = static_cast<float>((Me - m1) * log2e), down = exp2f(shift);
     s1 = sum(s1) + s_rest * down;
     t1 = sum(t1) + (s_rest == 0.f ? t_rest : fmaf(s_rest, shift, t_rest)) * down;
     if (lane == 0) {

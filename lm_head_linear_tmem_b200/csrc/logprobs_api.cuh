@@ -16,7 +16,14 @@ constexpr int kPlanSms = 148;
 // tile shape; single CTAs then spend half the tensor-core time of a pair on
 // the tile's empty rows.
 constexpr int kFewRows = BM;
-constexpr int kMaxRun = 16;
+// Longest runs (in tiles).  Longer ones mean fewer partial results, but CTAs that
+// share a column tile fall out of step and its weight rows leave L2 before the
+// last of them comes: 4096 x 4096 x 131072 took 2.47 ms with runs of 2, 2.54 with
+// 4 and 2.65 with 8 (8192 x 2048 x 32000: no difference).  Longer runs all the
+// same where the lists would take more than kMaxListBytes.
+constexpr int kMaxRun = 2;
+constexpr int kLongestRun = 16;
+constexpr size_t kMaxListBytes = size_t{512} << 20;
 
 struct ScorePlan {
   int cta_group;   // 1: 128 x 256 tiles of single CTAs, 2: 256-row tiles of pairs
@@ -24,31 +31,38 @@ struct ScorePlan {
   RunMap map;      // runs of column tiles
   int runs;
   int slots;       // partial results per row
-  int K;           // list length
+  int K;           // large logits kept for each row
+  int cap;         // entries of a list
   bool compact;    // rows without a token are left out of the GEMM
 };
 
-ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k) {
+// Tiles of 256 columns with softcap, whose long epilogue a 512-column tile exposes
+// (777 x 3584 x 256000: 1.06 against 1.11 ms), else as the forward's.
+ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k, bool softcap) {
   ScorePlan P{};
   P.K = static_cast<int>(std::min<int64_t>(top_k + kTopMargin, V));
+  P.cap = bf16 ? top_list_cap(P.K) : P.K;
   if (!bf16) {
     P.slots = static_cast<int>((V + kScoreCols - 1) / kScoreCols);
     return P;
   }
   P.cta_group = (o.cta_group == 1 || N <= kFewRows) ? 1 : 2;
-  P.bn = P.cta_group == 1 ? 256 : o.fwd_bn;
+  P.bn = P.cta_group == 1 || softcap ? 256 : o.fwd_bn;
   P.compact = N > kFewRows && o.fwd_compact;
   const int64_t unit_rows = BM * P.cta_group, workers = kPlanSms / P.cta_group;
   const int64_t mt = std::max<int64_t>((N + unit_rows - 1) / unit_rows, 1);
   const int64_t nt = (V + P.bn - 1) / P.bn;
-  // the longest runs: a power of two, four for every worker; then run_q (one for
-  // every worker) of each smaller length
-  int64_t n = 1;
-  while (n < kMaxRun && 2 * n * 4 * workers <= mt * nt) n *= 2;
+  // run_n: four of the longest runs for every worker at least; run_q (one for every
+  // worker) of each smaller length
   const int64_t q = (workers + mt - 1) / mt;
-  const int64_t c0 = n == 1 ? nt : std::max<int64_t>(0, (nt - q * (n - 1)) / n);
-  P.map = RunMap{static_cast<int>(n), static_cast<int>(c0), static_cast<int>(q)};
-  P.runs = P.map.of_tile(static_cast<int>(nt - 1)) + 1;
+  for (int64_t n = 1;; n *= 2) {
+    const int64_t c0 = n == 1 ? nt : std::max<int64_t>(0, (nt - q * (n - 1)) / n);
+    P.map = RunMap{static_cast<int>(n), static_cast<int>(c0), static_cast<int>(q)};
+    P.runs = P.map.of_tile(static_cast<int>(nt - 1)) + 1;
+    const size_t bytes = sizeof(TopEntry) * static_cast<size_t>(N) * 2 * P.runs * P.cap;
+    if (n >= kLongestRun || 2 * n * 4 * workers > mt * nt) break;
+    if (n >= kMaxRun && bytes <= kMaxListBytes) break;
+  }
   P.slots = 2 * P.runs;
   return P;
 }
@@ -70,7 +84,7 @@ ScoreLayout score_layout(const ScorePlan& P, int64_t N, int64_t H) {
   L.count = off;
   off = align_up(off + sizeof(int) * n * P.slots, 256);
   L.lists = off;
-  off = align_up(off + sizeof(TopEntry) * n * P.slots * P.K, 256);
+  off = align_up(off + sizeof(TopEntry) * n * P.slots * P.cap, 256);
   if (P.compact) {
     L.perm = off;
     off = align_up(off + 4 * n, 256);
@@ -223,12 +237,7 @@ flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout
                                   reinterpret_cast<uint32_t*>(w + L.seen)};
     return run_gemm<Epi, false, false>(d, o, P.bn, kFwdGemm, prob, ep, nullptr, ep, st);
   };
-  if (P.K <= kSmallTopList)
-    e = fin.softcap > 0.f ? score(ScoreEpi<true, kSmallTopList>{})
-                          : score(ScoreEpi<false, kSmallTopList>{});
-  else
-    e = fin.softcap > 0.f ? score(ScoreEpi<true, kMaxTopList>{})
-                          : score(ScoreEpi<false, kMaxTopList>{});
+  e = fin.softcap > 0.f ? score(ScoreEpi<true>{}) : score(ScoreEpi<false>{});
   if (e == cudaSuccess) e = run_finish<__nv_bfloat16>(hidden, weight, fin, st);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
 }
@@ -250,7 +259,7 @@ cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishA
   return launch(kSimt, st, [&] {
     score_simt_kernel<kRows><<<grid, kScoreThreads, score_simt_smem(kRows, a.H), st>>>(
         static_cast<const float*>(hidden), static_cast<const float*>(weight), a.N, a.H, a.V,
-        a.softcap, a.scale, a.slots, a.K, part, count, lists);
+        a.softcap, a.scale, a.slots, a.K, a.cap, part, count, lists);
   });
 }
 
@@ -266,7 +275,10 @@ size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dt
   if (dtype != FLCE_BF16 && dtype != FLCE_FP32) return 0;
   if (!score_sizes_ok(N, H, V, dtype)) return 0;
   if (top_k < 0 || top_k > FLCE_MAX_TOP_K || top_k > V) return 0;
-  return score_layout(score_plan(opts(), N, V, dtype == FLCE_BF16, top_k), N, H).end;
+  const bool bf16 = dtype == FLCE_BF16;
+  const Opts o = opts();
+  return std::max(score_layout(score_plan(o, N, V, bf16, top_k, false), N, H).end,
+                  score_layout(score_plan(o, N, V, bf16, top_k, true), N, H).end);
 }
 
 flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,
@@ -287,7 +299,7 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   if (N > 0 && (tokens == nullptr) != (logprobs == nullptr)) return FLCE_ERR_ARG;
   if (N > 0 && top_k > 0 && (top_logprobs == nullptr || top_ids == nullptr)) return FLCE_ERR_ARG;
   const bool bf16 = dtype == FLCE_BF16;
-  const ScorePlan P = score_plan(o, N, V, bf16, top_k);
+  const ScorePlan P = score_plan(o, N, V, bf16, top_k, softcap > 0.f);
   const ScoreLayout L = score_layout(P, N, H);
   if (workspace_bytes < L.end) return FLCE_ERR_WORKSPACE;
   DevInfo* d = nullptr;
@@ -313,6 +325,7 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   fin.nat = 1.0 / (temperature * static_cast<double>(scale));
   fin.slots = P.slots;
   fin.K = P.K;
+  fin.cap = P.cap;
   fin.top_k = top_k;
   fin.part = reinterpret_cast<const float4*>(w + L.part);
   fin.count = reinterpret_cast<const int*>(w + L.count);
