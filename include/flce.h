@@ -308,6 +308,42 @@ flce_status flce_logprobs_backward(const void* hidden, const void* weight, const
                                    float* d_hidden, float* d_weight, int32_t flags,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Embedding: rows of the [V, H] weight that the LM head shares with its
+ * embedding, and the weight's gradient.
+ *   out[i, :]      = scale * weight[ids[i], :]               (rounded once to the dtype)
+ *   d_weight[v, :] = scale * sum of d_out[i, :] over the tokens i with ids[i] == v
+ *                                                            (fp32, rounded once)
+ * A token whose id is ignore_index looks up zeros and has no gradient.  An id
+ * outside [0, V) that is not ignore_index is reported (bit 1 of the forward's
+ * status, FLCE_ERR_LABEL_RANGE from the backward's workspace) and treated the same way.
+ * A scale of NaN or infinity is FLCE_ERR_ARG.  H is any size from 1 to 2^20; rows of a
+ * multiple of 8 (or 4) elements with 16-byte-aligned pointers take vector accesses. */
+
+/* Forward.
+ *   dtype    of weight [V, H] and out [N, H]
+ *   status   optional device uint32[1]: the asynchronous error bits of this call
+ *            (1 = an id outside [0, V) that is not ignore_index), 0 if none.  NULL skips it. */
+flce_status flce_embedding_forward(const void* weight, const int64_t* ids, int64_t N, int64_t H,
+                                   int64_t V, int64_t ignore_index, float scale, int32_t dtype,
+                                   void* out, uint32_t* status, void* stream);
+
+/* Bytes of workspace of flce_embedding_backward (0 for invalid sizes). */
+size_t flce_embedding_workspace_bytes(int64_t N, int64_t H, int64_t V);
+
+/* Backward.
+ *   dtype        of d_out [N, H]
+ *   padding_idx  an id whose row gets no gradient (F.embedding's); negative: none
+ *   d_weight     device float[V * H], or bf16 with FLCE_DWEIGHT_BF16: overwritten (rows that no
+ *                token touches become zero) or, with FLCE_ACCUMULATE_DWEIGHT, added to (other
+ *                rows are not read or written): float(old) + gradient, rounded once.
+ *                Accumulating into the d_weight of flce_backward or flce_logprobs_backward
+ *                gives the gradient of tied weights.
+ * The result does not depend on timing: a row's tokens are added in a fixed order. */
+flce_status flce_embedding_backward(const void* d_out, const int64_t* ids, int64_t N, int64_t H,
+                                    int64_t V, int64_t ignore_index, int64_t padding_idx,
+                                    float scale, int32_t dtype, void* d_weight, int32_t flags,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the library-owned device buffer behind flce_forward_noalloc. */
 #define FLCE_NOALLOC_SCRATCH_BYTES (16u * 1024u * 1024u)
 

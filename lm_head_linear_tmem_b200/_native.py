@@ -29,6 +29,7 @@ BF16, FP32 = 0, 1
 ACCUMULATE_DHIDDEN, ACCUMULATE_DWEIGHT = 1, 2
 DHIDDEN_BF16, DWEIGHT_BF16 = 4, 8
 MAX_TOP_K = 32
+LABEL_RANGE = 3
 
 # flce_option values (include/flce.h)
 OPTIONS = {
@@ -61,6 +62,11 @@ SIGNATURES = {
     "flce_logprobs_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,
                                        c_f64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_size,
                                        c_vp]),
+    "flce_embedding_forward": (c_i32, [c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32, c_i32, c_vp,
+                                       c_vp, c_vp]),
+    "flce_embedding_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),
+    "flce_embedding_backward": (c_i32, [c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_i64, c_f32,
+                                        c_i32, c_vp, c_i32, c_vp, c_size, c_vp]),
     "flce_set_option": (c_i32, [c_i32, c_i64]),
     "flce_get_option": (c_i32, [c_i32, ctypes.POINTER(c_i64)]),
     "flce_forward_noalloc": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,

@@ -1,0 +1,435 @@
+// Kernels of the embedding that shares the LM head's weight: row lookup with a
+// scale, and the weight's gradient by sorted tokens.
+//   forward   out[i]  = scale * W[ids[i]]
+//   backward  dW[v]   = scale * sum over the tokens i with ids[i] = v, in order, of dOut[i]
+// (Arrays that an earlier launch of the call writes are read through plain pointers:
+// the launches overlap, so they are not constant for a kernel's lifetime.)
+// Both move memory and compute next to nothing: the lookup reads and writes N rows,
+// the gradient reads N rows and writes all V (overwritten) or those that the tokens
+// touch (accumulated).  Sums are fp32, rounded once.
+#pragma once
+
+#include "small_kernels.cuh"
+
+namespace flce {
+
+// ---------------------------------------------------------------- element groups
+// kVec consecutive elements of a row: 8 or 4 where rows and pointers allow vector
+// accesses of 16 or 8 bytes of bf16 (32 or 16 bytes of fp32), else 1.
+template <int kVec>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[kVec]) {
+  if constexpr (kVec == 1) {
+    v[0] = __bfloat162float(*p);
+  } else {
+    uint32_t w[kVec / 2];
+    if constexpr (kVec == 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x, w[1] = x.y;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <int kVec>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[kVec]) {
+  if constexpr (kVec == 1) {
+    v[0] = *p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec / 4; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(p)[i];
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    }
+  }
+}
+
+template <int kVec>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[kVec]) {
+  if constexpr (kVec == 1) {
+    *p = __float2bfloat16_rn(v[0]);
+  } else {
+    uint32_t w[kVec / 2];
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if constexpr (kVec == 8)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+}
+
+template <int kVec>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[kVec]) {
+  if constexpr (kVec == 1) {
+    *p = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] =
+          make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+
+// ---------------------------------------------------------------- lookup
+// `group` threads (a power of two) for each row, kLookupThreads / group rows per
+// block; each thread has up to four loads in flight.
+constexpr int kLookupThreads = 128;
+
+template <class T, int kVec>
+__global__ void __launch_bounds__(kLookupThreads)
+    embed_lookup_kernel(const T* __restrict__ weight, const int64_t* __restrict__ ids, int N, int H,
+                        int64_t V, int64_t ignore_index, float scale, int group,
+                        T* __restrict__ out, unsigned int* status) {
+  const int t = threadIdx.x & (group - 1);
+  const int row = blockIdx.x * (kLookupThreads / group) + threadIdx.x / group;
+  if (row >= N) return;
+  const int64_t id = ids[row];
+  const bool live = id != ignore_index && id >= 0 && id < V;
+  if (!live && id != ignore_index && t == 0 && status != nullptr)
+    atomicOr(status, kStatusLabelRange);
+  const T* src = weight + static_cast<size_t>(live ? id : 0) * H;
+  T* dst = out + static_cast<size_t>(row) * H;
+  const int chunks = H / kVec;
+  for (int c = t; c < chunks; c += 4 * group) {
+    float v[4][kVec];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (live && c + i * group < chunks) load_vec<kVec>(src + (c + i * group) * kVec, v[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + i * group >= chunks) break;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) v[i][k] = live ? v[i][k] * scale : 0.f;
+      store_vec<kVec>(dst + (c + i * group) * kVec, v[i]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sort
+// The tokens in (id, token) order.  Up to kSortMost tokens are sorted by one
+// block in shared memory (a stable radix sort, digits of `digit_bits` bits),
+// while the other blocks of the launch write the zeros of the weight rows that no
+// token touches: at 16384 tokens of a 131072 x 4096 bf16 gradient the sort is
+// hidden behind those writes.  More tokens than that go through the
+// label sort's kernels.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortMost = 16384;
+constexpr int kSortRounds = kSortMost / kSortThreads;  // tokens of a lane
+constexpr int kMaxDigits = 256;
+// two (key, index) buffers and the digit counts
+constexpr size_t kSortSmem =
+    2 * kSortMost * (sizeof(uint32_t) + sizeof(uint16_t)) + kMaxDigits * kSortWarps * sizeof(uint16_t);
+
+struct SortArgs {
+  const int64_t* ids;
+  int N;
+  int64_t V;
+  int64_t ignore_index;
+  int passes, digit_bits;
+  uint32_t* keys;       // [N] sorted ids; the first *n_valid are live
+  int* vals;            // [N] their tokens
+  long long* n_valid;
+  unsigned int* status;
+};
+
+__device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
+  uint32_t* key[2] = {reinterpret_cast<uint32_t*>(smem),
+                      reinterpret_cast<uint32_t*>(smem) + kSortMost};
+  uint16_t* val[2] = {reinterpret_cast<uint16_t*>(smem + 8 * kSortMost),
+                      reinterpret_cast<uint16_t*>(smem + 8 * kSortMost) + kSortMost};
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + 12 * kSortMost);  // [digit][warp]
+  __shared__ int warp_sum[kSortWarps];
+  __shared__ int live_sum;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  if (t == 0) live_sum = 0;
+  __syncthreads();
+  // a warp's tokens are consecutive: warp * per_warp + 32 * round + lane
+  const int rounds = (a.N + kSortThreads - 1) / kSortThreads;
+  const int per_warp = rounds * 32;
+  int live = 0;
+  for (int r = 0; r < rounds; ++r) {
+    const int i = warp * per_warp + r * 32 + lane;
+    uint32_t k = static_cast<uint32_t>(a.V);  // tokens left out sort behind the others
+    if (i < a.N) {
+      const int64_t id = a.ids[i];
+      if (id != a.ignore_index) {
+        if (id >= 0 && id < a.V) {
+          k = static_cast<uint32_t>(id);
+          ++live;
+        } else {
+          atomicOr(a.status, kStatusLabelRange);
+        }
+      }
+      key[0][i] = k;
+      val[0][i] = static_cast<uint16_t>(i);
+    }
+  }
+  atomicAdd(&live_sum, live);
+  const int digits = 1 << a.digit_bits, mask = digits - 1;
+  for (int ps = 0; ps < a.passes; ++ps) {
+    const int src = ps & 1, shift = ps * a.digit_bits;
+    for (int i = t; i < digits * kSortWarps; i += kSortThreads) cnt[i] = 0;
+    __syncthreads();
+    // digits of this warp's tokens, and each one's rank among the warp's equal ones
+    uint16_t rank[kSortRounds];
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+      if (r >= rounds) break;
+      const int i = warp * per_warp + r * 32 + lane;
+      const int d = i < a.N ? static_cast<int>((key[src][i] >> shift) & mask) : digits;
+      const unsigned peers = __match_any_sync(0xffffffffu, d);
+      const int before = d < digits ? cnt[d * kSortWarps + warp] : 0;
+      rank[r] = static_cast<uint16_t>(before + __popc(peers & ((1u << lane) - 1u)));
+      __syncwarp();
+      if (d < digits && (peers >> lane) == 1u)  // the last of its peers
+        cnt[d * kSortWarps + warp] = static_cast<uint16_t>(before + __popc(peers));
+      __syncwarp();
+    }
+    __syncthreads();
+    // exclusive prefix sum over (digit, warp)
+    const int n = digits * kSortWarps, each = (n + kSortThreads - 1) / kSortThreads;
+    int sum = 0;
+    for (int i = 0; i < each; ++i) sum += t * each + i < n ? cnt[t * each + i] : 0;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int i = 0; i < each; ++i)
+      if (t * each + i < n) {
+        const int c = cnt[t * each + i];
+        cnt[t * each + i] = static_cast<uint16_t>(base);  // below N <= 16384
+        base += c;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+      if (r >= rounds) break;
+      const int i = warp * per_warp + r * 32 + lane;
+      if (i < a.N) {
+        const uint32_t k = key[src][i];
+        const int to = cnt[((k >> shift) & mask) * kSortWarps + warp] + rank[r];
+        key[src ^ 1][to] = k;
+        val[src ^ 1][to] = val[src][i];
+      }
+    }
+    __syncthreads();
+  }
+  const int fin = a.passes & 1;
+  for (int i = t; i < a.N; i += kSortThreads) {
+    a.keys[i] = key[fin][i];
+    a.vals[i] = val[fin][i];
+  }
+  if (t == 0) *a.n_valid = live_sum;
+}
+
+// Zeros of the rows [v0, v1) of d_weight that no live token touches (padding_idx
+// counts as untouched).  Each range's touched rows are collected in a bit map by
+// reading all ids.  kVec 16-byte stores where rows are whole multiples of them.
+constexpr int kZeroRange = 32768;
+
+template <class TOut, bool kVec>
+__device__ __forceinline__ void zero_untouched(const int64_t* ids, int N, int64_t ignore_index,
+                                               int64_t padding_idx, int64_t v0, int64_t v1, int H,
+                                               TOut* d_weight, uint32_t* bits) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
+  for (; v0 < v1; v0 += kZeroRange) {
+    const int rows = static_cast<int>(v1 - v0 < kZeroRange ? v1 - v0 : kZeroRange);
+    __syncthreads();
+    for (int i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) bits[i] = 0u;
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += blockDim.x) {
+      const int64_t id = ids[i];
+      if (id >= v0 && id < v0 + rows && id != ignore_index && id != padding_idx)
+        atomicOr(&bits[(id - v0) >> 5], 1u << ((id - v0) & 31));
+    }
+    __syncthreads();
+    for (int r = warp; r < rows; r += warps) {
+      if ((bits[r >> 5] >> (r & 31)) & 1u) continue;
+      TOut* o = d_weight + static_cast<size_t>(v0 + r) * H;
+      if constexpr (kVec) {
+        const int n = H * static_cast<int>(sizeof(TOut)) / 16;
+        for (int c = lane; c < n; c += 32) reinterpret_cast<uint4*>(o)[c] = make_uint4(0, 0, 0, 0);
+      } else {
+        for (int c = lane; c < H; c += 32) o[c] = TOut(0.f);
+      }
+    }
+  }
+}
+
+// Block 0 sorts (if `sort`), the others (or all) zero their share of the rows.
+template <class TOut, bool kVec>
+__global__ void __launch_bounds__(kSortThreads)
+    embed_sort_zero_kernel(const SortArgs a, int sort, int zero, int64_t padding_idx, int H,
+                           TOut* __restrict__ d_weight) {
+  extern __shared__ __align__(16) uint8_t smem_dyn[];
+  griddep_launch_dependents();
+  if (sort && blockIdx.x == 0) {
+    sort_block(a, smem_dyn);
+    return;
+  }
+  if (!zero) return;
+  const int64_t b = static_cast<int>(blockIdx.x) - sort, n = static_cast<int>(gridDim.x) - sort;
+  zero_untouched<TOut, kVec>(a.ids, a.N, a.ignore_index, padding_idx, a.V * b / n,
+                             a.V * (b + 1) / n, H, d_weight, reinterpret_cast<uint32_t*>(smem_dyn));
+}
+
+// ---------------------------------------------------------------- sums
+// Segments of kEmbedSeg sorted tokens x kEmbedThreads * kVec columns.  A run of one
+// id inside a segment is finished there; a run that crosses segments leaves its
+// pieces in part[segment][slot] (slot 0: the segment's first run, begun earlier;
+// slot 1: its last run, going on), and embed_join adds them in order.
+constexpr int kEmbedSeg = 32;
+constexpr int kEmbedThreads = 128;
+
+// scale * sum into row v: stored, or added to what is there, in one rounding.
+template <class TOut, int kVec>
+__device__ __forceinline__ void embed_put(TOut* d_weight, uint32_t v, int H, int col,
+                                          const float (&sum)[kVec], float scale, int accumulate) {
+  TOut* o = d_weight + static_cast<size_t>(v) * H + col;
+  float x[kVec];
+  if (accumulate) {
+    if constexpr (kVec == 1) {
+      x[0] = static_cast<float>(*o);
+    } else {
+      load_vec<kVec>(o, x);
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) x[k] = fmaf(scale, sum[k], x[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) x[k] = scale * sum[k];
+  }
+  store_vec<kVec>(o, x);
+}
+
+template <class TIn, class TOut, int kVec>
+__global__ void __launch_bounds__(kEmbedThreads)
+    embed_segments_kernel(const uint32_t* keys, const int* vals,
+                          const long long* n_valid, const TIn* __restrict__ d_out,
+                          int H, uint32_t padding, float scale, int accumulate, TOut* d_weight,
+                          float* part) {
+  __shared__ uint32_t key[kEmbedSeg + 2];  // with the tokens before and behind
+  __shared__ int val[kEmbedSeg];
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long nv = *n_valid;
+  const long long s0 = static_cast<long long>(blockIdx.x) * kEmbedSeg;
+  if (s0 >= nv) return;
+  const int n = static_cast<int>(nv - s0 < kEmbedSeg ? nv - s0 : kEmbedSeg);
+  constexpr uint32_t kNone = 0xffffffffu;
+  for (int i = threadIdx.x; i < kEmbedSeg + 2; i += kEmbedThreads) {
+    const long long j = s0 + i - 1;
+    key[i] = (j >= 0 && j < nv) ? keys[j] : kNone;
+    if (i < n) val[i] = vals[s0 + i];
+  }
+  __syncthreads();
+  const int col = (blockIdx.y * kEmbedThreads + threadIdx.x) * kVec;
+  if (col >= H) return;
+  float* seg = part + static_cast<size_t>(blockIdx.x) * 2 * H + col;
+  const TIn* src = d_out + col;
+  float sum[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) sum[k] = 0.f;
+  bool begun_before = key[0] == key[1];
+  constexpr int kAhead = 8;  // loads in flight
+  for (int b = 0; b < n; b += kAhead) {
+    float x[kAhead][kVec];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (b + i < n) load_vec<kVec>(src + static_cast<size_t>(val[b + i]) * H, x[i]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (b + i >= n) break;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) sum[k] += x[i][k];
+      const uint32_t id = key[b + i + 1];
+      if (id == key[b + i + 2] && b + i + 1 < n) continue;  // the run goes on here
+      const bool goes_on = id == key[b + i + 2];            // ... in the next segment
+      if (begun_before)
+        store_vec<kVec>(seg, sum);
+      else if (goes_on)
+        store_vec<kVec>(seg + H, sum);
+      else if (id != padding)
+        embed_put<TOut, kVec>(d_weight, id, H, col, sum, scale, accumulate);
+      begun_before = false;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) sum[k] = 0.f;
+    }
+  }
+}
+
+// The pieces of runs that cross segments, by the block of the segment where the
+// run begins: kJoinWays groups of threads each add a stretch of the pieces, and
+// their sums are added in order.
+constexpr int kJoinWays = 8;
+constexpr int kJoinCols = 32;  // threads along the columns
+
+template <class TOut, int kVec>
+__global__ void __launch_bounds__(kJoinWays * kJoinCols)
+    embed_join_kernel(const uint32_t* keys, const long long* n_valid,
+                      int H, uint32_t padding, float scale, int accumulate, TOut* d_weight,
+                      const float* part) {
+  __shared__ float sums[kJoinWays][kJoinCols][kVec + 1];
+  griddep_wait();
+  const long long nv = *n_valid;
+  const long long s0 = static_cast<long long>(blockIdx.x) * kEmbedSeg;
+  const long long end = s0 + kEmbedSeg;
+  if (end >= nv) return;  // nothing behind this segment
+  const uint32_t id = keys[end - 1];
+  if (id == padding || keys[end] != id) return;     // its last run ends here
+  if (s0 > 0 && keys[s0 - 1] == id) return;         // it began in an earlier segment
+  // the run's end: the first key behind `end` that is larger
+  long long lo = end, hi = nv;
+  while (lo < hi) {
+    const long long mid = (lo + hi) / 2;
+    if (keys[mid] == id) lo = mid + 1; else hi = mid;
+  }
+  // pieces: this segment's slot 1, then slot 0 of the segments up to the run's end
+  const int pieces = 1 + static_cast<int>((lo - 1) / kEmbedSeg - blockIdx.x);
+  const int x = threadIdx.x, y = threadIdx.y;
+  const int col = (blockIdx.y * kJoinCols + x) * kVec;
+  float sum[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) sum[k] = 0.f;
+  if (col < H) {
+    const int p0 = static_cast<int>(static_cast<long long>(pieces) * y / kJoinWays);
+    const int p1 = static_cast<int>(static_cast<long long>(pieces) * (y + 1) / kJoinWays);
+#pragma unroll 4
+    for (int p = p0; p < p1; ++p) {
+      float v[kVec];
+      load_vec<kVec>(part + (static_cast<size_t>(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * H + col,
+                     v);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) sum[k] += v[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) sums[y][x][k] = sum[k];
+  __syncthreads();
+  if (y != 0 || col >= H) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWays; ++w)
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sum[k] += sums[w][x][k];
+  embed_put<TOut, kVec>(d_weight, id, H, col, sum, scale, accumulate);
+}
+
+}  // namespace flce

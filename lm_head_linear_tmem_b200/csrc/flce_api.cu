@@ -28,12 +28,14 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <set>
 #include <utility>
 #include <vector>
 
 #include "../../include/flce.h"
+#include "embedding_kernels.cuh"
 #include "logprob_kernels.cuh"
 
 namespace flce {
@@ -1172,6 +1174,7 @@ flce_status backward_any(const void* hidden, const void* weight, const int64_t* 
 }  // namespace flce
 
 #include "logprobs_api.cuh"
+#include "embedding_api.cuh"
 
 using namespace flce;
 
