@@ -29,10 +29,10 @@ int bit_length(uint64_t v) {
   return n;
 }
 
-// Workspace: header | sorted ids and tokens, live count | pieces of runs | and, for
+// Workspace: header (status word, number of joins at 4) | sorted ids and tokens, live count | pieces of runs | and, for
 // more tokens than one block sorts, the label sort's arrays.
 struct EmbedLayout {
-  size_t keys, vals, n_valid, part, keys1, vals1, perm, labels_c, block_valid, hist, end;
+  size_t keys, vals, n_valid, joins, part, keys1, vals1, perm, labels_c, block_valid, hist, end;
 };
 
 EmbedLayout embed_layout(int64_t N, int64_t H) {
@@ -47,6 +47,7 @@ EmbedLayout embed_layout(int64_t N, int64_t H) {
   L.keys = take(4 * n);
   L.vals = take(4 * n);
   L.n_valid = take(8);
+  L.joins = take(4 * ((n + kEmbedSeg - 1) / kEmbedSeg));
   L.part = take(((n + kEmbedSeg - 1) / kEmbedSeg) * 2 * static_cast<size_t>(H) * sizeof(float));
   if (N > kSortMost) {
     const size_t nblk = (n + kCompactThreads - 1) / kCompactThreads;
@@ -96,6 +97,9 @@ cudaError_t launch_dependent(Kern k, dim3 grid, dim3 block, cudaStream_t st, Arg
   return le != cudaSuccess ? le : e;
 }
 
+// Blocks of embed_join along its list.
+constexpr unsigned kJoinBlocks = 64;
+
 template <class TIn, class TOut, int kVec>
 cudaError_t run_sums(const void* d_out, int64_t N, int H, int64_t padding, float scale,
                      int accumulate, void* d_weight, char* w, const EmbedLayout& L,
@@ -104,6 +108,8 @@ cudaError_t run_sums(const void* d_out, int64_t N, int H, int64_t padding, float
   const int* vals = reinterpret_cast<const int*>(w + L.vals);
   const long long* n_valid = reinterpret_cast<const long long*>(w + L.n_valid);
   float* part = reinterpret_cast<float*>(w + L.part);
+  int* join_count = reinterpret_cast<int*>(w + 4);
+  int* joins = reinterpret_cast<int*>(w + L.joins);
   // an id that no live token has, where there is no padding_idx
   const uint32_t pad = padding >= 0 ? static_cast<uint32_t>(padding) : 0xffffffffu;
   const unsigned segs = static_cast<unsigned>((N + kEmbedSeg - 1) / kEmbedSeg);
@@ -113,11 +119,14 @@ cudaError_t run_sums(const void* d_out, int64_t N, int H, int64_t padding, float
   cudaError_t e = launch_dependent(embed_segments_kernel<TIn, TOut, kVec>,
                                    dim3(segs, cols(kEmbedThreads)), dim3(kEmbedThreads), st, keys,
                                    vals, n_valid, static_cast<const TIn*>(d_out), H, pad, scale,
-                                   accumulate, static_cast<TOut*>(d_weight), part);
+                                   accumulate, static_cast<TOut*>(d_weight), part, join_count,
+                                   joins);
   if (e == cudaSuccess)
-    e = launch_dependent(embed_join_kernel<TOut, kVec>, dim3(segs, cols(kJoinCols)),
-                         dim3(kJoinCols, kJoinWays), st, keys, n_valid, H, pad, scale, accumulate,
-                         static_cast<TOut*>(d_weight), static_cast<const float*>(part));
+    e = launch_dependent(embed_join_kernel<TOut, kVec>,
+                         dim3(std::min(segs, kJoinBlocks), cols(kJoinCols)),
+                         dim3(kJoinCols, kJoinWays), st, keys, n_valid, H, scale, accumulate,
+                         static_cast<TOut*>(d_weight), static_cast<const float*>(part),
+                         static_cast<const int*>(join_count), static_cast<const int*>(joins));
   return e;
 }
 
@@ -260,7 +269,7 @@ flce_status flce_embedding_backward(const void* d_out, const int64_t* ids, int64
   if (s != FLCE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(workspace);
-  cudaError_t e = cudaMemsetAsync(w, 0, 16, st);  // status word
+  cudaError_t e = cudaMemsetAsync(w, 0, 16, st);  // status word, number of joins
   if (e != cudaSuccess) return cuda_fail(e);
   SortArgs a{};
   a.ids = ids;

@@ -159,11 +159,18 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
   const int rounds = (a.N + kSortThreads - 1) / kSortThreads;
   const int per_warp = rounds * 32;
   int live = 0;
-  for (int r = 0; r < rounds; ++r) {
+  int64_t id_of[kSortRounds];  // all loads in flight
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int i = warp * per_warp + r * 32 + lane;
+    id_of[r] = r < rounds && i < a.N ? a.ids[i] : a.ignore_index;
+  }
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
     const int i = warp * per_warp + r * 32 + lane;
     uint32_t k = static_cast<uint32_t>(a.V);  // tokens left out sort behind the others
-    if (i < a.N) {
-      const int64_t id = a.ids[i];
+    if (r < rounds && i < a.N) {
+      const int64_t id = id_of[r];
       if (id != a.ignore_index) {
         if (id >= 0 && id < a.V) {
           k = static_cast<uint32_t>(id);
@@ -180,7 +187,8 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
   const int digits = 1 << a.digit_bits, mask = digits - 1;
   for (int ps = 0; ps < a.passes; ++ps) {
     const int src = ps & 1, shift = ps * a.digit_bits;
-    for (int i = t; i < digits * kSortWarps; i += kSortThreads) cnt[i] = 0;
+    for (int i = t; i < digits * kSortWarps / 8; i += kSortThreads)  // (digits >= 2)
+      reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     // digits of this warp's tokens, and each one's rank among the warp's equal ones
     uint16_t rank[kSortRounds];
@@ -210,8 +218,14 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int base = incl - sum;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    int before = warp_sum[lane];  // the sums of the warps up to `lane`
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    before = __shfl_sync(0xffffffffu, before, (warp + 31) & 31);
+    int base = incl - sum + (warp > 0 ? before : 0);
     for (int i = 0; i < each; ++i)
       if (t * each + i < n) {
         const int c = cnt[t * each + i];
@@ -295,27 +309,40 @@ __global__ void __launch_bounds__(kSortThreads)
 // Segments of kEmbedSeg sorted tokens x kEmbedThreads * kVec columns.  A run of one
 // id inside a segment is finished there; a run that crosses segments leaves its
 // pieces in part[segment][slot] (slot 0: the segment's first run, begun earlier;
-// slot 1: its last run, going on), and embed_join adds them in order.
+// slot 1: its last run, going on), and embed_join adds them in order.  The segment
+// where such a run begins enters itself in the list of joins, each a task of its
+// own, whatever the list's order.
 constexpr int kEmbedSeg = 32;
 constexpr int kEmbedThreads = 128;
 
-// scale * sum into row v: stored, or added to what is there, in one rounding.
+// scale * sum into row v: stored, or added to what is there.  Into fp32 by
+// reductions that return nothing: no thread waits for the old value, and each
+// element gets one addition per call, so the result stays reproducible (waiting,
+// a segment of 32 different ids took 26 us).
 template <class TOut, int kVec>
 __device__ __forceinline__ void embed_put(TOut* d_weight, uint32_t v, int H, int col,
                                           const float (&sum)[kVec], float scale, int accumulate) {
   TOut* o = d_weight + static_cast<size_t>(v) * H + col;
   float x[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) x[k] = scale * sum[k];
   if (accumulate) {
-    if constexpr (kVec == 1) {
-      x[0] = static_cast<float>(*o);
+    if constexpr (std::is_same_v<TOut, float>) {
+      if constexpr (kVec == 1) {
+        atomicAdd(o, x[0]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec / 4; ++i)
+          atomicAdd(reinterpret_cast<float4*>(o) + i,
+                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+      }
+      return;
     } else {
-      load_vec<kVec>(o, x);
+      float old[kVec];
+      load_vec<kVec>(o, old);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x[k] = fmaf(scale, sum[k], old[k]);
     }
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) x[k] = fmaf(scale, sum[k], x[k]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) x[k] = scale * sum[k];
   }
   store_vec<kVec>(o, x);
 }
@@ -325,7 +352,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
     embed_segments_kernel(const uint32_t* keys, const int* vals,
                           const long long* n_valid, const TIn* __restrict__ d_out,
                           int H, uint32_t padding, float scale, int accumulate, TOut* d_weight,
-                          float* part) {
+                          float* part, int* join_count, int* joins) {
   __shared__ uint32_t key[kEmbedSeg + 2];  // with the tokens before and behind
   __shared__ int val[kEmbedSeg];
   griddep_wait();
@@ -338,9 +365,15 @@ __global__ void __launch_bounds__(kEmbedThreads)
   for (int i = threadIdx.x; i < kEmbedSeg + 2; i += kEmbedThreads) {
     const long long j = s0 + i - 1;
     key[i] = (j >= 0 && j < nv) ? keys[j] : kNone;
-    if (i < n) val[i] = vals[s0 + i];
+    if (i < kEmbedSeg) val[i] = vals[s0 + min(i, n - 1)];  // (past the end: the last one again)
   }
   __syncthreads();
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    const uint32_t last = key[n];
+    const bool whole = key[0] == last && key[1] == last;  // began in an earlier segment
+    if (n == kEmbedSeg && key[n + 1] == last && !whole && last != padding)
+      joins[atomicAdd(join_count, 1)] = static_cast<int>(blockIdx.x);
+  }
   const int col = (blockIdx.y * kEmbedThreads + threadIdx.x) * kVec;
   if (col >= H) return;
   float* seg = part + static_cast<size_t>(blockIdx.x) * 2 * H + col;
@@ -354,7 +387,7 @@ __global__ void __launch_bounds__(kEmbedThreads)
     float x[kAhead][kVec];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (b + i < n) load_vec<kVec>(src + static_cast<size_t>(val[b + i]) * H, x[i]);
+      load_vec<kVec>(src + static_cast<size_t>(val[b + i]) * H, x[i]);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (b + i >= n) break;
@@ -376,60 +409,61 @@ __global__ void __launch_bounds__(kEmbedThreads)
   }
 }
 
-// The pieces of runs that cross segments, by the block of the segment where the
-// run begins: kJoinWays groups of threads each add a stretch of the pieces, and
-// their sums are added in order.
+// The runs that cross segments: for each entry of the list, kJoinWays groups of
+// threads each add a stretch of the run's pieces, and their sums are added in order.
 constexpr int kJoinWays = 8;
 constexpr int kJoinCols = 32;  // threads along the columns
 
 template <class TOut, int kVec>
 __global__ void __launch_bounds__(kJoinWays * kJoinCols)
-    embed_join_kernel(const uint32_t* keys, const long long* n_valid,
-                      int H, uint32_t padding, float scale, int accumulate, TOut* d_weight,
-                      const float* part) {
+    embed_join_kernel(const uint32_t* keys, const long long* n_valid, int H, float scale,
+                      int accumulate, TOut* d_weight, const float* part, const int* join_count,
+                      const int* joins) {
   __shared__ float sums[kJoinWays][kJoinCols][kVec + 1];
   griddep_wait();
+  const int count = *join_count;
   const long long nv = *n_valid;
-  const long long s0 = static_cast<long long>(blockIdx.x) * kEmbedSeg;
-  const long long end = s0 + kEmbedSeg;
-  if (end >= nv) return;  // nothing behind this segment
-  const uint32_t id = keys[end - 1];
-  if (id == padding || keys[end] != id) return;     // its last run ends here
-  if (s0 > 0 && keys[s0 - 1] == id) return;         // it began in an earlier segment
-  // the run's end: the first key behind `end` that is larger
-  long long lo = end, hi = nv;
-  while (lo < hi) {
-    const long long mid = (lo + hi) / 2;
-    if (keys[mid] == id) lo = mid + 1; else hi = mid;
-  }
-  // pieces: this segment's slot 1, then slot 0 of the segments up to the run's end
-  const int pieces = 1 + static_cast<int>((lo - 1) / kEmbedSeg - blockIdx.x);
-  const int x = threadIdx.x, y = threadIdx.y;
+  const int x = threadIdx.x, y = threadIdx.y, t = y * kJoinCols + x;
   const int col = (blockIdx.y * kJoinCols + x) * kVec;
-  float sum[kVec];
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) sum[k] = 0.f;
-  if (col < H) {
-    const int p0 = static_cast<int>(static_cast<long long>(pieces) * y / kJoinWays);
-    const int p1 = static_cast<int>(static_cast<long long>(pieces) * (y + 1) / kJoinWays);
-#pragma unroll 4
-    for (int p = p0; p < p1; ++p) {
-      float v[kVec];
-      load_vec<kVec>(part + (static_cast<size_t>(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * H + col,
-                     v);
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) sum[k] += v[k];
+  for (int j = blockIdx.x; j < count; j += gridDim.x) {
+    const int seg = joins[j];
+    const long long end = static_cast<long long>(seg + 1) * kEmbedSeg;
+    const uint32_t id = keys[end - 1];
+    // pieces: this segment's slot 1, then slot 0 of every later segment that starts
+    // with the id (all threads look at once: a search by halves waits for 14 loads)
+    int pieces = 1;
+    for (bool more = true; more;) {
+      const long long first = end + static_cast<long long>(pieces - 1 + t) * kEmbedSeg;
+      const int n = __syncthreads_count(first < nv && keys[first] == id);
+      pieces += n;
+      more = n == kJoinWays * kJoinCols;
     }
+    float sum[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sum[k] = 0.f;
+    if (col < H) {
+      const int p0 = static_cast<int>(static_cast<long long>(pieces) * y / kJoinWays);
+      const int p1 = static_cast<int>(static_cast<long long>(pieces) * (y + 1) / kJoinWays);
+#pragma unroll 4
+      for (int p = p0; p < p1; ++p) {
+        float v[kVec];
+        load_vec<kVec>(part + (static_cast<size_t>(seg + p) * 2 + (p == 0 ? 1 : 0)) * H + col, v);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) sum[k] += v[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sums[y][x][k] = sum[k];
+    __syncthreads();
+    if (y == 0 && col < H) {
+#pragma unroll
+      for (int w = 1; w < kJoinWays; ++w)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) sum[k] += sums[w][x][k];
+      embed_put<TOut, kVec>(d_weight, id, H, col, sum, scale, accumulate);
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) sums[y][x][k] = sum[k];
-  __syncthreads();
-  if (y != 0 || col >= H) return;
-#pragma unroll
-  for (int w = 1; w < kJoinWays; ++w)
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) sum[k] += sums[w][x][k];
-  embed_put<TOut, kVec>(d_weight, id, H, col, sum, scale, accumulate);
 }
 
 }  // namespace flce
