@@ -128,9 +128,12 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMost = 16384;
 constexpr int kSortRounds = kSortMost / kSortThreads;  // tokens of a lane
 constexpr int kMaxDigits = 256;
+// Digit counts: a row of a count per warp for each digit, 17 words apart so that
+// a warp's lanes, which read the same column of different rows, use all banks.
+constexpr int kCntRow = kSortWarps + 2;
 // two (key, index) buffers and the digit counts
 constexpr size_t kSortSmem =
-    2 * kSortMost * (sizeof(uint32_t) + sizeof(uint16_t)) + kMaxDigits * kSortWarps * sizeof(uint16_t);
+    2 * kSortMost * (sizeof(uint32_t) + sizeof(uint16_t)) + kMaxDigits * kCntRow * sizeof(uint16_t);
 
 struct SortArgs {
   const int64_t* ids;
@@ -149,7 +152,7 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
                       reinterpret_cast<uint32_t*>(smem) + kSortMost};
   uint16_t* val[2] = {reinterpret_cast<uint16_t*>(smem + 8 * kSortMost),
                       reinterpret_cast<uint16_t*>(smem + 8 * kSortMost) + kSortMost};
-  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + 12 * kSortMost);  // [digit][warp]
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + 12 * kSortMost);  // [digit][kCntRow]
   __shared__ int warp_sum[kSortWarps];
   __shared__ int live_sum;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -187,8 +190,8 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
   const int digits = 1 << a.digit_bits, mask = digits - 1;
   for (int ps = 0; ps < a.passes; ++ps) {
     const int src = ps & 1, shift = ps * a.digit_bits;
-    for (int i = t; i < digits * kSortWarps / 8; i += kSortThreads)  // (digits >= 2)
-      reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = t; i < digits * kCntRow / 2; i += kSortThreads)
+      reinterpret_cast<uint32_t*>(cnt)[i] = 0u;
     __syncthreads();
     // digits of this warp's tokens, and each one's rank among the warp's equal ones
     uint16_t rank[kSortRounds];
@@ -197,19 +200,35 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
       if (r >= rounds) break;
       const int i = warp * per_warp + r * 32 + lane;
       const int d = i < a.N ? static_cast<int>((key[src][i] >> shift) & mask) : digits;
-      const unsigned peers = __match_any_sync(0xffffffffu, d);
-      const int before = d < digits ? cnt[d * kSortWarps + warp] : 0;
+      // lanes with the same digit, a ballot for each bit (__match_any_sync took
+      // five times as long with 32 warps at it)
+      unsigned peers = __ballot_sync(0xffffffffu, d < digits);
+      for (int b = 0; b < a.digit_bits; ++b) {
+        const bool bit = (d >> b) & 1;
+        const unsigned ones = __ballot_sync(0xffffffffu, bit);
+        peers &= bit ? ones : ~ones;
+      }
+      const int before = d < digits ? cnt[d * kCntRow + warp] : 0;
       rank[r] = static_cast<uint16_t>(before + __popc(peers & ((1u << lane) - 1u)));
       __syncwarp();
       if (d < digits && (peers >> lane) == 1u)  // the last of its peers
-        cnt[d * kSortWarps + warp] = static_cast<uint16_t>(before + __popc(peers));
+        cnt[d * kCntRow + warp] = static_cast<uint16_t>(before + __popc(peers));
       __syncwarp();
     }
     __syncthreads();
     // exclusive prefix sum over (digit, warp)
-    const int n = digits * kSortWarps, each = (n + kSortThreads - 1) / kSortThreads;
+    // (four threads for each digit, eight warps' counts each)
+    static_assert(kSortWarps == 32 && kMaxDigits * 4 == kSortThreads, "a thread's counts");
+    uint32_t* mine = reinterpret_cast<uint32_t*>(cnt + (t >> 2) * kCntRow + (t & 3) * 8);
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
     int sum = 0;
-    for (int i = 0; i < each; ++i) sum += t * each + i < n ? cnt[t * each + i] : 0;
+    if (t < digits * 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = mine[i];
+        sum += static_cast<int>((c[i] & 0xffffu) + (c[i] >> 16));
+      }
+    }
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -226,12 +245,14 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
     }
     before = __shfl_sync(0xffffffffu, before, (warp + 31) & 31);
     int base = incl - sum + (warp > 0 ? before : 0);
-    for (int i = 0; i < each; ++i)
-      if (t * each + i < n) {
-        const int c = cnt[t * each + i];
-        cnt[t * each + i] = static_cast<uint16_t>(base);  // below N <= 16384
-        base += c;
+    if (t < digits * 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // (offsets stay below N <= 16384)
+        const uint32_t first = base, second = base + (c[i] & 0xffffu);
+        mine[i] = first | second << 16;
+        base = static_cast<int>(second + (c[i] >> 16));
       }
+    }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kSortRounds; ++r) {
@@ -239,7 +260,7 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
       const int i = warp * per_warp + r * 32 + lane;
       if (i < a.N) {
         const uint32_t k = key[src][i];
-        const int to = cnt[((k >> shift) & mask) * kSortWarps + warp] + rank[r];
+        const int to = cnt[((k >> shift) & mask) * kCntRow + warp] + rank[r];
         key[src ^ 1][to] = k;
         val[src ^ 1][to] = val[src][i];
       }
