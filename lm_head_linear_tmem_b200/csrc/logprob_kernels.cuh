@@ -436,6 +436,7 @@ __global__ void __launch_bounds__(kScoreThreads)
 #pragma unroll
     for (int c = 0; c < kC; ++c)  // columns past the block's end repeat its last one
       w[c] = weight + static_cast<size_t>(v0 + min(c0 + c, cols - 1)) * H;
+#pragma unroll 4
     for (int k = lane; k < H; k += 32) {
       float wv[kC];
 #pragma unroll
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kScoreThreads)
 // with their fp64 values.  The backward recomputes the uncorrected logits: it gets
 // the uncorrected lse and entropy (`saved`), with which its 1 - p of a
 // dominant token keeps its leading digits.
-constexpr int kGroups = 128;  // of a row's lists, for the lower bound of the K-th best
+constexpr int kGroups = 64;  // of a row's lists, for the lower bound of the K-th best
 constexpr int kMaxHits = 512;
 constexpr int kMaxHitSlots = 256;
 
@@ -600,15 +601,14 @@ __device__ __forceinline__ float gemm_softcap<float>(float z, float softcap) {
   return capped(z, softcap);
 }
 
-// kFinishThreads: 128, or 512 where there are so few rows that one row's latency
-// (its K + 1 dot products above all) is the kernel's time.
+// kFinishThreads: by the rows and the dot products of a row (see run_finish).
 template <class T, int kFinishThreads>
 __global__ void __launch_bounds__(kFinishThreads)
     score_finish_kernel(const T* __restrict__ hidden, const T* __restrict__ weight,
                         const FinishArgs a) {
   constexpr int kWarps = kFinishThreads / 32;
-  __shared__ Stats wst[kWarps];
-  __shared__ float tmaxs[kFinishThreads], bound_sh;
+  __shared__ float wm[kWarps], ws[kWarps], wt[kWarps], bound_sh;
+  __shared__ __align__(16) float tmaxs[kFinishThreads];
   __shared__ int n_hits, n_hit_slots;
   __shared__ int hit_slots[kMaxHitSlots];  // slot, and its entries in the top byte
   __shared__ TopEntry hits[kMaxHits], wbest[2][kWarps];
@@ -654,12 +654,10 @@ __global__ void __launch_bounds__(kFinishThreads)
     stats_merge(st, Stats{v.x, v.y, v.z});
     tmax = fmaxf(tmax, v.w);
   }
+  float wmax = st.m;
 #pragma unroll
-  for (int o = 16; o >= 1; o /= 2)
-    stats_merge(st, Stats{__shfl_down_sync(0xffffffffu, st.m, o),
-                          __shfl_down_sync(0xffffffffu, st.s, o),
-                          __shfl_down_sync(0xffffffffu, st.t, o)});
-  if (lane == 0) wst[warp] = st;
+  for (int o = 16; o >= 1; o /= 2) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, o));
+  if (lane == 0) wm[warp] = wmax;
 
   // ---- the K best entries.  The K-th largest of the groups' maxima is a lower
   // bound of the K-th best (each is a logit of its own), and about K lists have
@@ -683,12 +681,27 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   if (t < kGroups) {
     int above = 0, ties = 0;
-#pragma unroll 16
-    for (int i = 0; i < kGroups; ++i) {
-      above += tmaxs[i] > gmax ? 1 : 0;
-      ties += tmaxs[i] == gmax ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < kGroups; i += 4) {
+      const float4 g = *reinterpret_cast<const float4*>(tmaxs + i);
+      above += (g.x > gmax) + (g.y > gmax) + (g.z > gmax) + (g.w > gmax);
+      ties += (g.x == gmax) + (g.y == gmax) + (g.z == gmax) + (g.w == gmax);
     }
     if (above < a.K && above + ties >= a.K) bound_sh = gmax;  // one value whoever writes it
+  }
+  // the row's statistics: all slots' sums at the largest maximum, added in a fixed order
+  float M = wm[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, wm[w]);
+  stats_rebase(st, M, exp2f(st.m - M));
+#pragma unroll
+  for (int o = 16; o >= 1; o /= 2) {
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+    st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
+  }
+  if (lane == 0) {
+    ws[warp] = st.s;
+    wt[warp] = st.t;
   }
   __syncthreads();
   const float bound = bound_sh;
@@ -778,9 +791,12 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   __syncthreads();
   if (warp == 0) {
-    st = wst[0];
+    st = Stats{M, ws[0], wt[0]};
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) stats_merge(st, wst[w]);
+    for (int w = 1; w < kWarps; ++w) {
+      st.s += ws[w];
+      st.t += wt[w];
+    }
     auto sum = [](float v) {
 #pragma unroll
       for (int o = 16; o >= 1; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -788,7 +804,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     };
     const double Me = static_cast<double>(st.m) * a.nat;  // the GEMM's maximum
     double m1 = Me;
-    float s_rest = 0.f, t_rest = 0.f;
+    float s_rest = 0.f, t_rest = 0.f, z_sum = 0.f, dz_sum = 0.f;
     for (int c = lane; c < a.K; c += 32) {
       if (ids[c] < 0) continue;
       const float L = a.softcap > 0.f ? gemm_softcap<T>(za[c], a.softcap) : za[c];
@@ -797,14 +813,28 @@ __global__ void __launch_bounds__(kFinishThreads)
       s_rest += e;
       t_rest = fmaf(e, d, t_rest);
       m1 = fmax(m1, xe[c]);
+      z_sum += fabsf(za[c]);
+      dz_sum += static_cast<float>(fabs(zx[c]) - fabs(static_cast<double>(za[c])));
     }
     // what the listed ones leave (a NaN sum stays NaN)
     s_rest = st.s - sum(s_rest);
     t_rest = st.t - sum(t_rest);
     if (s_rest < 0.f) s_rest = 0.f;
     if (t_rest > 0.f) t_rest = 0.f;
-#pragma unroll
-    for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    // The share that the truncation took of the listed logits it took, on the
+    // average, of the others too; their mean (by probability) is known, so their
+    // sum is moved by that.  At most what truncating every partial sum can take.
+    z_sum = sum(z_sum);
+    dz_sum = sum(dz_sum);
+    if (a.softcap == 0.f && s_rest > 0.f && z_sum > 0.f) {
+      const float share = fminf(fmaxf(dz_sum / z_sum, 0.f), a.H * 0x1p-27f);
+      const float mean = st.m + t_rest / s_rest;  // log2 units
+      const float up = exp2f(share * mean);
+      if (up < 2.f && up > 0.5f) {
+        t_rest = fmaf(s_rest, share * mean, t_rest) * up;
+        s_rest *= up;
+      }
+    }
     // ... and with their fp64 values, at the largest of those
     float s1 = 0.f, t1 = 0.f;
     for (int c = lane; c < a.K; c += 32) {

@@ -126,9 +126,12 @@ flce_status check_score(const Opts& o, const void* hidden, const void* weight, i
   return FLCE_OK;
 }
 
-// Rows up to which score_finish gives each row a block of 512 threads (two for
-// every SM) instead of 128.
+// Threads that score_finish gives each row: 512 up to kFinishFewRows rows (two for
+// every SM), where a row's latency is what counts (32 rows, K = 24: 55 us with 128);
+// else 64, or 128 from kFinishManyDots dot products (8192 rows, K = 4: 70 against 93 us;
+// 4096 rows, K = 12: 187 against 140).
 constexpr int kFinishFewRows = 2 * kPlanSms;
+constexpr int kFinishManyDots = 8;
 
 template <class T, int kThreads>
 cudaError_t run_finish_with(const void* hidden, const void* weight, const FinishArgs& a,
@@ -153,8 +156,9 @@ cudaError_t run_finish_with(const void* hidden, const void* weight, const Finish
 template <class T>
 cudaError_t run_finish(const void* hidden, const void* weight, const FinishArgs& a,
                        cudaStream_t st) {
-  return a.N <= kFinishFewRows ? run_finish_with<T, 512>(hidden, weight, a, st)
-                               : run_finish_with<T, 128>(hidden, weight, a, st);
+  if (a.N <= kFinishFewRows) return run_finish_with<T, 512>(hidden, weight, a, st);
+  return a.K + 1 >= kFinishManyDots ? run_finish_with<T, 128>(hidden, weight, a, st)
+                                    : run_finish_with<T, 64>(hidden, weight, a, st);
 }
 
 flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout& L,
