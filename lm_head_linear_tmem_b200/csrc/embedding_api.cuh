@@ -23,12 +23,6 @@ bool embed_sizes_ok(int64_t N, int64_t H, int64_t V) {
   return N >= 0 && V >= 1 && H >= 1 && N <= kMaxDim && V <= kMaxDim && H <= (1 << 20);
 }
 
-int bit_length(uint64_t v) {
-  int n = 0;
-  for (; v != 0; v >>= 1) ++n;
-  return n;
-}
-
 // Workspace: header (status word, number of joins at 4) | sorted ids and tokens, live count | pieces of runs | and, for
 // more tokens than one block sorts, the label sort's arrays.
 struct EmbedLayout {
@@ -135,6 +129,8 @@ cudaError_t run_embed_backward(DevInfo* d, const void* d_out, bool in_bf16, cons
                                int H, int64_t padding, float scale, int accumulate,
                                void* d_weight, char* w, const EmbedLayout& L, cudaStream_t st) {
   const bool one_block = a.N <= kSortMost;
+  uint32_t* sorted_keys = reinterpret_cast<uint32_t*>(w + L.keys);
+  int* sorted_vals = reinterpret_cast<int*>(w + L.vals);
   cudaError_t e = cudaSuccess;
   if (!one_block) {
     const int n = a.N, nblk = (n + kCompactThreads - 1) / kCompactThreads;
@@ -142,10 +138,10 @@ cudaError_t run_embed_backward(DevInfo* d, const void* d_out, bool in_bf16, cons
     int64_t* labels_c = reinterpret_cast<int64_t*>(w + L.labels_c);
     int* block_valid = reinterpret_cast<int*>(w + L.block_valid);
     int* hist = reinterpret_cast<int*>(w + L.hist);
-    uint32_t* keys[2] = {a.keys, reinterpret_cast<uint32_t*>(w + L.keys1)};
-    int* vals[2] = {a.vals, reinterpret_cast<int*>(w + L.vals1)};
+    uint32_t* keys[2] = {sorted_keys, reinterpret_cast<uint32_t*>(w + L.keys1)};
+    int* vals[2] = {sorted_vals, reinterpret_cast<int*>(w + L.vals1)};
     const int passes = (bit_length(static_cast<uint64_t>(a.V - 1)) + 7) / 8;
-    const int first = passes & 1;  // so that the last pass ends in a.keys
+    const int first = passes & 1;  // so that the last pass ends in sorted_keys
     e = launch(kHelper, st, [&] {
       compact_count_kernel<<<nblk, kCompactThreads, 0, st>>>(a.ids, n, a.ignore_index, a.V,
                                                              a.status, block_valid);
@@ -188,7 +184,8 @@ cudaError_t run_embed_backward(DevInfo* d, const void* d_out, bool in_bf16, cons
     const size_t smem = one_block ? kSortSmem : kZeroRange / 8;
     const int grid = accumulate ? 1 : d->sms;
     e = launch(kHelper, st, [&] {
-      k<<<grid, kSortThreads, smem, st>>>(a, one_block ? 1 : 0, accumulate ? 0 : 1, padding, H,
+      k<<<grid, kSortThreads, smem, st>>>(a, sorted_keys, sorted_vals, one_block ? 1 : 0,
+                                          accumulate ? 0 : 1, padding, H,
                                           static_cast<TOut*>(d_weight));
     });
     if (e != cudaSuccess) return e;
@@ -276,11 +273,7 @@ flce_status flce_embedding_backward(const void* d_out, const int64_t* ids, int64
   a.N = static_cast<int>(N);
   a.V = V;
   a.ignore_index = ignore_index;
-  const int bits = bit_length(static_cast<uint64_t>(V));  // V itself marks tokens left out
-  a.passes = (bits + 7) / 8;
-  a.digit_bits = (bits + a.passes - 1) / a.passes;
-  a.keys = reinterpret_cast<uint32_t*>(w + L.keys);
-  a.vals = reinterpret_cast<int*>(w + L.vals);
+  sort_by_id(a);
   a.n_valid = reinterpret_cast<long long*>(w + L.n_valid);
   a.status = ws_status(w);
   const int acc = (flags & FLCE_ACCUMULATE_DWEIGHT) != 0 ? 1 : 0;

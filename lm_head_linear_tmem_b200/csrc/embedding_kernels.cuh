@@ -9,7 +9,7 @@
 // touch (accumulated).  Sums are fp32, rounded once.
 #pragma once
 
-#include "small_kernels.cuh"
+#include "row_order.cuh"
 
 namespace flce {
 
@@ -116,165 +116,7 @@ __global__ void __launch_bounds__(kLookupThreads)
   }
 }
 
-// ---------------------------------------------------------------- sort
-// The tokens in (id, token) order.  Up to kSortMost tokens are sorted by one
-// block in shared memory (a stable radix sort, digits of `digit_bits` bits),
-// while the other blocks of the launch write the zeros of the weight rows that no
-// token touches: at 16384 tokens of a 131072 x 4096 bf16 gradient the sort is
-// hidden behind those writes.  More tokens than that go through the
-// label sort's kernels.
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortMost = 16384;
-constexpr int kSortRounds = kSortMost / kSortThreads;  // tokens of a lane
-constexpr int kMaxDigits = 256;
-// Digit counts: a row of a count per warp for each digit, 17 words apart so that
-// a warp's lanes, which read the same column of different rows, use all banks.
-constexpr int kCntRow = kSortWarps + 2;
-// two (key, index) buffers and the digit counts
-constexpr size_t kSortSmem =
-    2 * kSortMost * (sizeof(uint32_t) + sizeof(uint16_t)) + kMaxDigits * kCntRow * sizeof(uint16_t);
-
-struct SortArgs {
-  const int64_t* ids;
-  int N;
-  int64_t V;
-  int64_t ignore_index;
-  int passes, digit_bits;
-  uint32_t* keys;       // [N] sorted ids; the first *n_valid are live
-  int* vals;            // [N] their tokens
-  long long* n_valid;
-  unsigned int* status;
-};
-
-__device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem) {
-  uint32_t* key[2] = {reinterpret_cast<uint32_t*>(smem),
-                      reinterpret_cast<uint32_t*>(smem) + kSortMost};
-  uint16_t* val[2] = {reinterpret_cast<uint16_t*>(smem + 8 * kSortMost),
-                      reinterpret_cast<uint16_t*>(smem + 8 * kSortMost) + kSortMost};
-  uint16_t* cnt = reinterpret_cast<uint16_t*>(smem + 12 * kSortMost);  // [digit][kCntRow]
-  __shared__ int warp_sum[kSortWarps];
-  __shared__ int live_sum;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t == 0) live_sum = 0;
-  __syncthreads();
-  // a warp's tokens are consecutive: warp * per_warp + 32 * round + lane
-  const int rounds = (a.N + kSortThreads - 1) / kSortThreads;
-  const int per_warp = rounds * 32;
-  int live = 0;
-  int64_t id_of[kSortRounds];  // all loads in flight
-#pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int i = warp * per_warp + r * 32 + lane;
-    id_of[r] = r < rounds && i < a.N ? a.ids[i] : a.ignore_index;
-  }
-#pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int i = warp * per_warp + r * 32 + lane;
-    uint32_t k = static_cast<uint32_t>(a.V);  // tokens left out sort behind the others
-    if (r < rounds && i < a.N) {
-      const int64_t id = id_of[r];
-      if (id != a.ignore_index) {
-        if (id >= 0 && id < a.V) {
-          k = static_cast<uint32_t>(id);
-          ++live;
-        } else {
-          atomicOr(a.status, kStatusLabelRange);
-        }
-      }
-      key[0][i] = k;
-      val[0][i] = static_cast<uint16_t>(i);
-    }
-  }
-  atomicAdd(&live_sum, live);
-  const int digits = 1 << a.digit_bits, mask = digits - 1;
-  for (int ps = 0; ps < a.passes; ++ps) {
-    const int src = ps & 1, shift = ps * a.digit_bits;
-    for (int i = t; i < digits * kCntRow / 2; i += kSortThreads)
-      reinterpret_cast<uint32_t*>(cnt)[i] = 0u;
-    __syncthreads();
-    // digits of this warp's tokens, and each one's rank among the warp's equal ones
-    uint16_t rank[kSortRounds];
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-      if (r >= rounds) break;
-      const int i = warp * per_warp + r * 32 + lane;
-      const int d = i < a.N ? static_cast<int>((key[src][i] >> shift) & mask) : digits;
-      // lanes with the same digit, a ballot for each bit (__match_any_sync took
-      // five times as long with 32 warps at it)
-      unsigned peers = __ballot_sync(0xffffffffu, d < digits);
-      for (int b = 0; b < a.digit_bits; ++b) {
-        const bool bit = (d >> b) & 1;
-        const unsigned ones = __ballot_sync(0xffffffffu, bit);
-        peers &= bit ? ones : ~ones;
-      }
-      const int before = d < digits ? cnt[d * kCntRow + warp] : 0;
-      rank[r] = static_cast<uint16_t>(before + __popc(peers & ((1u << lane) - 1u)));
-      __syncwarp();
-      if (d < digits && (peers >> lane) == 1u)  // the last of its peers
-        cnt[d * kCntRow + warp] = static_cast<uint16_t>(before + __popc(peers));
-      __syncwarp();
-    }
-    __syncthreads();
-    // exclusive prefix sum over (digit, warp)
-    // (four threads for each digit, eight warps' counts each)
-    static_assert(kSortWarps == 32 && kMaxDigits * 4 == kSortThreads, "a thread's counts");
-    uint32_t* mine = reinterpret_cast<uint32_t*>(cnt + (t >> 2) * kCntRow + (t & 3) * 8);
-    uint32_t c[4] = {0u, 0u, 0u, 0u};
-    int sum = 0;
-    if (t < digits * 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = mine[i];
-        sum += static_cast<int>((c[i] & 0xffffu) + (c[i] >> 16));
-      }
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int before = warp_sum[lane];  // the sums of the warps up to `lane`
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
-    }
-    before = __shfl_sync(0xffffffffu, before, (warp + 31) & 31);
-    int base = incl - sum + (warp > 0 ? before : 0);
-    if (t < digits * 4) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // (offsets stay below N <= 16384)
-        const uint32_t first = base, second = base + (c[i] & 0xffffu);
-        mine[i] = first | second << 16;
-        base = static_cast<int>(second + (c[i] >> 16));
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-      if (r >= rounds) break;
-      const int i = warp * per_warp + r * 32 + lane;
-      if (i < a.N) {
-        const uint32_t k = key[src][i];
-        const int to = cnt[((k >> shift) & mask) * kCntRow + warp] + rank[r];
-        key[src ^ 1][to] = k;
-        val[src ^ 1][to] = val[src][i];
-      }
-    }
-    __syncthreads();
-  }
-  const int fin = a.passes & 1;
-  for (int i = t; i < a.N; i += kSortThreads) {
-    a.keys[i] = key[fin][i];
-    a.vals[i] = val[fin][i];
-  }
-  if (t == 0) *a.n_valid = live_sum;
-}
-
+// ---------------------------------------------------------------- zeros
 // Zeros of the rows [v0, v1) of d_weight that no live token touches (padding_idx
 // counts as untouched).  Each range's touched rows are collected in a bit map by
 // reading all ids.  kVec 16-byte stores where rows are whole multiples of them.
@@ -309,15 +151,19 @@ __device__ __forceinline__ void zero_untouched(const int64_t* ids, int N, int64_
   }
 }
 
-// Block 0 sorts (if `sort`), the others (or all) zero their share of the rows.
+// Block 0 sorts (if `sort`), the others (or all) zero their share of the rows: at
+// 16384 tokens of a 131072 x 4096 bf16 gradient the sort is hidden behind those writes.
 template <class TOut, bool kVec>
 __global__ void __launch_bounds__(kSortThreads)
-    embed_sort_zero_kernel(const SortArgs a, int sort, int zero, int64_t padding_idx, int H,
-                           TOut* __restrict__ d_weight) {
+    embed_sort_zero_kernel(const SortArgs a, uint32_t* keys, int* vals, int sort, int zero,
+                           int64_t padding_idx, int H, TOut* __restrict__ d_weight) {
   extern __shared__ __align__(16) uint8_t smem_dyn[];
   griddep_launch_dependents();
   if (sort && blockIdx.x == 0) {
-    sort_block(a, smem_dyn);
+    sort_block(a, smem_dyn, [&](int i, uint32_t key, int token, int) {
+      keys[i] = key;
+      vals[i] = token;
+    });
     return;
   }
   if (!zero) return;

@@ -37,6 +37,7 @@
 #include "../../include/flce.h"
 #include "embedding_kernels.cuh"
 #include "logprob_kernels.cuh"
+#include "row_order.cuh"
 
 namespace flce {
 namespace {
@@ -554,6 +555,67 @@ cudaError_t run_gemm(DevInfo* d, const Opts& o, int bn, int kind, const GemmProb
                                                               ctas_out);
 }
 
+// ---------------------------------------------------------------- row order
+int bit_length(uint64_t v) {
+  int n = 0;
+  for (; v != 0; v >>= 1) ++n;
+  return n;
+}
+
+void sort_by_id(SortArgs& a) {
+  const int bits = bit_length(static_cast<uint64_t>(a.V));  // V itself marks tokens left out
+  a.by_id = 1;
+  a.passes = (bits + 7) / 8;
+  a.digit_bits = (bits + a.passes - 1) / a.passes;
+}
+
+// order_rows for at most kSortMost rows; the rows' order by label if `by_label`.
+cudaError_t order_rows(const int64_t* labels, int n, int64_t V, int64_t ignore_index,
+                       bool by_label, const float* lse, int* perm, int64_t* labels_c,
+                       float* lse_c, long long* n_valid, unsigned int* status, cudaStream_t st) {
+  SortArgs a{};
+  a.ids = labels;
+  a.N = n;
+  a.V = V;
+  a.ignore_index = ignore_index;
+  a.passes = a.digit_bits = 1;
+  if (by_label) sort_by_id(a);
+  a.n_valid = n_valid;
+  a.status = status;
+  const cudaError_t e = set_smem_attr(order_rows_kernel, kSortSmem);
+  if (e != cudaSuccess) return e;
+  return launch(kHelper, st, [&] {
+    order_rows_kernel<<<1, kSortThreads, kSortSmem, st>>>(a, lse, perm, labels_c, lse_c);
+  });
+}
+
+// The valid rows first, in row order (the forward's and the scoring operator's
+// compaction): perm, labels_c and *n_valid.
+cudaError_t compact_rows(const int64_t* labels, int n, int64_t V, int64_t ignore_index, int* perm,
+                         int64_t* labels_c, int* block_valid, long long* n_valid,
+                         unsigned int* status, cudaStream_t st) {
+  if (n <= kSortMost)
+    return order_rows(labels, n, V, ignore_index, false, nullptr, perm, labels_c, nullptr, n_valid,
+                      status, st);
+  const int cblk = (n + kCompactThreads - 1) / kCompactThreads;
+  cudaError_t e = launch(kHelper, st, [&] {
+    compact_count_kernel<<<cblk, kCompactThreads, 0, st>>>(labels, n, ignore_index, V, status,
+                                                           block_valid);
+  });
+  if (e == cudaSuccess)
+    e = launch(kHelper, st, [&] {
+      exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(block_valid, cblk, n_valid);
+    });
+  if (e == cudaSuccess)
+    e = launch(kHelper, st, [&] {
+      compact_scatter_kernel<<<cblk, kCompactThreads, 0, st>>>(labels, nullptr, n, ignore_index,
+                                                               block_valid, n_valid, perm,
+                                                               labels_c, nullptr, V, nullptr,
+                                                               nullptr);
+    });
+  return e;
+}
+
 // Rows of B (K-major) one CTA stages per bank and K-block.
 uint32_t b_box_rows(const Opts& o) { return static_cast<uint32_t>(BN / o.cta_group); }
 
@@ -590,21 +652,8 @@ flce_status forward_bf16(DevInfo* d, const Opts& o, const void* hidden, const vo
     int* block_valid = reinterpret_cast<int*>(w + L.block_valid);
     n_valid_c = reinterpret_cast<long long*>(w + L.n_valid_c);
     void* hidden_c = w + L.hidden_c;
-    const int cblk = (n + kCompactThreads - 1) / kCompactThreads;
-    e = launch(kHelper, st, [&] {
-      compact_count_kernel<<<cblk, kCompactThreads, 0, st>>>(labels, n, ignore_index, V,
-                                                             ws_status(ws), block_valid);
-    });
-    if (e == cudaSuccess)
-      e = launch(kHelper, st, [&] {
-        exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(block_valid, cblk, n_valid_c);
-      });
-    if (e == cudaSuccess)
-      e = launch(kHelper, st, [&] {
-        compact_scatter_kernel<<<cblk, kCompactThreads, 0, st>>>(
-            labels, nullptr, n, ignore_index, block_valid, n_valid_c, perm, labels_c, nullptr, V,
-            nullptr, nullptr);
-      });
+    e = compact_rows(labels, n, V, ignore_index, perm, labels_c, block_valid, n_valid_c,
+                     ws_status(ws), st);
     if (e == cudaSuccess)
       e = launch(kHelper, st, [&] {
         gather_rows_kernel<<<n, 256, 0, st>>>(static_cast<const uint4*>(hidden),
@@ -717,6 +766,24 @@ flce_status forward_fp32(DevInfo* d, const void* hidden, const void* weight,
 }
 
 // ---------------------------------------------------------------- backward
+// Columns of a gradient tile of a chunk of `rows` tokens x `cols` columns: the
+// option's, or 256 where tiles of 512 are so few that one of them is the launch's
+// time.  A tile's time goes as its K-blocks times its columns; a launch takes at
+// least its longest tile's and its share of all.  400 x 1000 x 10007: the dHidden
+// tiles (157 K-blocks) are four of 512 or eight of 256 columns, for 74 CTA pairs:
+// 106 or 60 us.
+int grad_tile_cols(const Opts& o, int sms, int64_t rows, int64_t cols, int64_t H, bool dh,
+                   bool dw) {
+  if (o.grad_bn != 512) return o.grad_bn;
+  const auto time = [&](int64_t bn) {
+    const int64_t nt = (H + bn - 1) / bn;
+    const int64_t kh = dh ? (cols + BK - 1) / BK : 0, kw = dw ? (rows + BK - 1) / BK : 0;
+    const int64_t all = ((rows + 255) / 256 * kh + (cols + 255) / 256 * kw) * nt * bn;
+    return std::max(std::max(kh, kw) * bn, all / std::max(1, sms / 2));
+  };
+  return 4 * time(512) > 5 * time(256) ? 256 : 512;
+}
+
 // rg (scoring operator): per-row upstream gradients instead of the loss's scalar.
 flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const void* weight,
                           const int64_t* labels, const float* lse, int64_t N, int64_t H,
@@ -761,51 +828,57 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
     void* hidden_c = w + BL.hidden_c;
     const int n = static_cast<int>(N);
     const int nblk = (n + kCompactThreads - 1) / kCompactThreads;
-    cudaError_t e = launch(kHelper, st, [&] {
-      compact_count_kernel<<<nblk, kCompactThreads, 0, st>>>(labels, n, ignore_index, V,
-                                                             ws_status(ws), block_valid);
-    });
-    if (e == cudaSuccess)
+    cudaError_t e = cudaSuccess;
+    if (n <= kSortMost) {
+      e = order_rows(labels, n, V, ignore_index, true, lse, perm, labels_c, lse_c, n_valid_c,
+                     ws_status(ws), st);
+    } else {
       e = launch(kHelper, st, [&] {
-        exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(block_valid, nblk, n_valid_c);
-      });
-    uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(w + BL.keys0),
-                         reinterpret_cast<uint32_t*>(w + BL.keys1)};
-    int* vals[2] = {reinterpret_cast<int*>(w + BL.vals0), reinterpret_cast<int*>(w + BL.vals1)};
-    if (e == cudaSuccess)
-      e = launch(kHelper, st, [&] {
-        compact_scatter_kernel<<<nblk, kCompactThreads, 0, st>>>(
-            labels, lse, n, ignore_index, block_valid, n_valid_c, perm, labels_c, lse_c, V,
-            keys[0], vals[0]);
-      });
-    // Valid rows in (label, token) order: keys are labels in [0, V), so
-    // ceil(bits(V - 1) / 8) passes of 8 bits sort them.
-    int key_bits = 0;
-    while (((V - 1) >> key_bits) != 0) ++key_bits;
-    const int passes = (key_bits + 7) / 8;
-    int* hist = reinterpret_cast<int*>(w + BL.hist);
-    for (int ps = 0; ps < passes && e == cudaSuccess; ++ps) {
-      const int src = ps & 1, shift = 8 * ps;
-      e = launch(kHelper, st, [&] {
-        radix_hist_kernel<<<nblk, kCompactThreads, 0, st>>>(keys[src], n_valid_c, shift, nblk,
-                                                              hist);
+        compact_count_kernel<<<nblk, kCompactThreads, 0, st>>>(labels, n, ignore_index, V,
+                                                               ws_status(ws), block_valid);
       });
       if (e == cudaSuccess)
         e = launch(kHelper, st, [&] {
-          exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(hist, kRadixBuckets * nblk,
-                                                               nullptr);
+          exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(block_valid, nblk, n_valid_c);
         });
+      uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(w + BL.keys0),
+                           reinterpret_cast<uint32_t*>(w + BL.keys1)};
+      int* vals[2] = {reinterpret_cast<int*>(w + BL.vals0), reinterpret_cast<int*>(w + BL.vals1)};
       if (e == cudaSuccess)
         e = launch(kHelper, st, [&] {
-          radix_scatter_kernel<<<nblk, kCompactThreads, 0, st>>>(
-              keys[src], vals[src], keys[src ^ 1], vals[src ^ 1], n_valid_c, shift, nblk, hist);
+          compact_scatter_kernel<<<nblk, kCompactThreads, 0, st>>>(
+              labels, lse, n, ignore_index, block_valid, n_valid_c, perm, labels_c, lse_c, V,
+              keys[0], vals[0]);
+        });
+      // Valid rows in (label, token) order: keys are labels in [0, V), so
+      // ceil(bits(V - 1) / 8) passes of 8 bits sort them.
+      int key_bits = 0;
+      while (((V - 1) >> key_bits) != 0) ++key_bits;
+      const int passes = (key_bits + 7) / 8;
+      int* hist = reinterpret_cast<int*>(w + BL.hist);
+      for (int ps = 0; ps < passes && e == cudaSuccess; ++ps) {
+        const int src = ps & 1, shift = 8 * ps;
+        e = launch(kHelper, st, [&] {
+          radix_hist_kernel<<<nblk, kCompactThreads, 0, st>>>(keys[src], n_valid_c, shift, nblk,
+                                                                hist);
+        });
+        if (e == cudaSuccess)
+          e = launch(kHelper, st, [&] {
+            exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(hist, kRadixBuckets * nblk,
+                                                                 nullptr);
+          });
+        if (e == cudaSuccess)
+          e = launch(kHelper, st, [&] {
+            radix_scatter_kernel<<<nblk, kCompactThreads, 0, st>>>(
+                keys[src], vals[src], keys[src ^ 1], vals[src ^ 1], n_valid_c, shift, nblk, hist);
+          });
+      }
+      if (e == cudaSuccess)
+        e = launch(kHelper, st, [&] {
+          apply_label_order_kernel<<<nblk, kCompactThreads, 0, st>>>(
+              keys[passes & 1], vals[passes & 1], lse, n_valid_c, perm, labels_c, lse_c);
         });
     }
-    if (e == cudaSuccess)
-      e = launch(kHelper, st, [&] {
-        apply_label_order_kernel<<<nblk, kCompactThreads, 0, st>>>(
-            keys[passes & 1], vals[passes & 1], lse, n_valid_c, perm, labels_c, lse_c);
-      });
     if (e == cudaSuccess)
       e = launch(kHelper, st, [&] {
         gather_rows_kernel<<<n, 256, 0, st>>>(
@@ -979,7 +1052,7 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
 
       const GemmProblem ph{&t_g_k, &t_w_mn, &t_dh, rows, H, gh};
       const GemmProblem pw{&t_g_mn, &t_hid_mn, &t_dw, cols, H, gw};
-      const int gbn = o.grad_bn;
+      const int gbn = grad_tile_cols(o, d->sms, rows, cols, H, want_dh, want_dw);
       int ctas = 0;
       if (want_dh && want_dw && o.fuse) {
         // 2) + 3) in one launch: the dWeight tiles fill the dHidden grid's last wave

@@ -174,21 +174,8 @@ flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout
     int* block_valid = reinterpret_cast<int*>(w + L.block_valid);
     n_valid_c = reinterpret_cast<long long*>(w + L.n_valid_c);
     void* hidden_c = w + L.hidden_c;
-    const int cblk = (n + kCompactThreads - 1) / kCompactThreads;
-    e = launch(kHelper, st, [&] {
-      compact_count_kernel<<<cblk, kCompactThreads, 0, st>>>(tokens, n, fin.ignore_index, fin.V,
-                                                             fin.status, block_valid);
-    });
-    if (e == cudaSuccess)
-      e = launch(kHelper, st, [&] {
-        exclusive_scan_kernel<<<1, kCompactThreads, 0, st>>>(block_valid, cblk, n_valid_c);
-      });
-    if (e == cudaSuccess)
-      e = launch(kHelper, st, [&] {
-        compact_scatter_kernel<<<cblk, kCompactThreads, 0, st>>>(
-            tokens, nullptr, n, fin.ignore_index, block_valid, n_valid_c, perm, tokens_c, nullptr,
-            fin.V, nullptr, nullptr);
-      });
+    e = compact_rows(tokens, n, fin.V, fin.ignore_index, perm, tokens_c, block_valid, n_valid_c,
+                     fin.status, st);
     if (e == cudaSuccess)
       e = launch(kHelper, st, [&] {
         gather_rows_kernel<<<n, 256, 0, st>>>(static_cast<const uint4*>(hidden), H / 8, n, perm,

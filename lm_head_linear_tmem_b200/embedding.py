@@ -16,15 +16,16 @@ from . import _native
 from .flce import _DTYPES, _lib, _ptr, _stream, check_workspace, on_device, status
 
 
+_ID_DTYPES = (torch.int64, torch.int32, torch.int16, torch.uint8, torch.int8)
+
+
 def _ids(ids: torch.Tensor, device) -> torch.Tensor:
-    if not ids.is_cuda or ids.device != device:
+    if ids.device != device:
         raise ValueError("ids must be a CUDA tensor on the weight's device")
-    if ids.is_floating_point() or ids.is_complex() or ids.dtype == torch.bool:
+    if ids.dtype not in _ID_DTYPES:
         raise TypeError("ids must be integers")
-    y = ids.reshape(-1)
-    if y.dtype != torch.int64:
-        y = y.to(torch.int64)
-    return y.contiguous()
+    y = ids if ids.dim() == 1 else ids.reshape(-1)
+    return y.to(torch.int64).contiguous() if y.dtype != torch.int64 else y.contiguous()
 
 
 def embedding_forward(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,

@@ -62,10 +62,10 @@ def on_device(device: torch.device):
 
 
 def _prep(hidden: torch.Tensor, weight: torch.Tensor, labels: Optional[torch.Tensor]):
-    given = [t for t in (hidden, weight, labels) if t is not None]
-    if not all(t.is_cuda for t in given):
+    dev = hidden.device
+    if not (dev.type == "cuda" and weight.is_cuda and (labels is None or labels.is_cuda)):
         raise ValueError("hidden, weight and labels must be CUDA tensors")
-    if any(t.device != hidden.device for t in given):
+    if weight.device != dev or (labels is not None and labels.device != dev):
         raise ValueError("hidden, weight and labels must be on one device")
     if hidden.dtype not in _DTYPES or weight.dtype != hidden.dtype:
         raise TypeError("hidden and weight must both be bfloat16 or both float32")
