@@ -94,7 +94,7 @@ __device__ __forceinline__ bool better(TopEntry a, TopEntry b) {
 
 // Entries of a run's list: room for the K best and K new ones (see scan), and some
 // more so that this limit seldom counts.
-constexpr int top_list_cap(int K) { return 2 * K + 8; }
+constexpr int top_list_cap(int K) { return 2 * K + 24; }
 constexpr int kMaxTopCap = top_list_cap(kMaxTopList);
 
 template <bool kSoftcap>
@@ -194,7 +194,7 @@ struct ScoreEpi {
       else
         hi = x;
       // (NaN bounds, from infinities, end the search where it is)
-      const bool done = (n >= K && n <= K + K / 2 + 2) || !(hi > bound);
+      const bool done = (n >= K && n <= 2 * K + 4) || !(hi > bound);
       if (__all_sync(0xffffffffu, done)) break;
       if (!done) {
         x = bound > -CUDART_INF_F ? 0.5f * bound + 0.5f * hi : x - step;
@@ -220,7 +220,7 @@ struct ScoreEpi {
     };
     int n = find(S.above);
     float kth = -CUDART_INF_F;
-    if (__any_sync(0xffffffffu, n > K + 8)) {
+    if (__any_sync(0xffffffffu, n > 2 * K + 4)) {
       // a run's start, before any CTA has seen enough of the row (or logits that
       // rise with the id): all but the block's own best would be for nothing
       kth = near_kth(r, K, mx);
@@ -410,13 +410,15 @@ struct ScoreEpi {
 constexpr int kScoreCols = 256;
 constexpr int kScoreThreads = 256;
 
-template <int kRows>
+// kVec: 4 where H is a multiple of 4 (hidden and weight rows are then 16-byte
+// aligned), else 1.
+template <int kRows, int kVec>
 __global__ void __launch_bounds__(kScoreThreads)
     score_simt_kernel(const float* __restrict__ hidden, const float* __restrict__ weight, int N,
                       int H, int V, float softcap, float scale, int slots, int K, int cap,
                       float4* __restrict__ part, int* __restrict__ count,
                       TopEntry* __restrict__ lists) {
-  extern __shared__ float sh[];
+  extern __shared__ __align__(16) float sh[];
   float* hs = sh;               // [kRows][H]
   float* zs = sh + kRows * H;   // [kRows][kScoreCols]
   const int row0 = blockIdx.y * kRows, v0 = blockIdx.x * kScoreCols;
@@ -436,16 +438,27 @@ __global__ void __launch_bounds__(kScoreThreads)
 #pragma unroll
     for (int c = 0; c < kC; ++c)  // columns past the block's end repeat its last one
       w[c] = weight + static_cast<size_t>(v0 + min(c0 + c, cols - 1)) * H;
-#pragma unroll 4
-    for (int k = lane; k < H; k += 32) {
-      float wv[kC];
+#pragma unroll 2
+    for (int k = lane * kVec; k < H; k += 32 * kVec) {
+      float wv[kC][kVec];
 #pragma unroll
-      for (int c = 0; c < kC; ++c) wv[c] = w[c][k];
+      for (int c = 0; c < kC; ++c) {
+        if constexpr (kVec == 4)
+          *reinterpret_cast<float4*>(wv[c]) = *reinterpret_cast<const float4*>(w[c] + k);
+        else
+          wv[c][0] = w[c][k];
+      }
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        const float h = hs[r * H + k];
+        float h[kVec];
+        if constexpr (kVec == 4)
+          *reinterpret_cast<float4*>(h) = *reinterpret_cast<const float4*>(hs + r * H + k);
+        else
+          h[0] = hs[r * H + k];
 #pragma unroll
-        for (int c = 0; c < kC; ++c) acc[r][c] = fmaf(h, wv[c], acc[r][c]);
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[r][c] = fmaf(h[i], wv[c][i], acc[r][c]);
       }
     }
 #pragma unroll

@@ -244,11 +244,12 @@ template <int kRows>
 cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishArgs& a,
                            float4* part, int* count, TopEntry* lists, cudaStream_t st) {
   static_assert(2 * (kSimtMaxH + kScoreCols) * sizeof(float) <= kScoreSimtSmem, "two rows fit");
-  const cudaError_t e = set_smem_attr(score_simt_kernel<kRows>, kScoreSimtSmem);
+  const auto k = a.H % 4 == 0 ? score_simt_kernel<kRows, 4> : score_simt_kernel<kRows, 1>;
+  const cudaError_t e = set_smem_attr(k, kScoreSimtSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.slots), static_cast<unsigned>((a.N + kRows - 1) / kRows));
   return launch(kSimt, st, [&] {
-    score_simt_kernel<kRows><<<grid, kScoreThreads, score_simt_smem(kRows, a.H), st>>>(
+    k<<<grid, kScoreThreads, score_simt_smem(kRows, a.H), st>>>(
         static_cast<const float*>(hidden), static_cast<const float*>(weight), a.N, a.H, a.V,
         a.softcap, a.scale, a.slots, a.K, a.cap, part, count, lists);
   });
