@@ -329,6 +329,30 @@ int64_t bwd_chunks(const Opts& o, int64_t N, int64_t V) {
   return ((N + c.tc - 1) / c.tc) * ((V + c.vc - 1) / c.vc);
 }
 
+// Ranges that the scoring operator's backward cuts the vocabulary dimension of a
+// chunk's dHidden product into, each with an fp32 block of its own that dh_scatter adds
+// in order: where the token rows make too few tiles for the SMs, the time would be that of one
+// tile's K loop over the whole vocabulary chunk.  1: not cut.
+// 400 x 1000 x 10007 (8 tiles of 157 K-blocks): the launch took 71 us uncut.
+constexpr int kPlanPairs = 74;  // CTA pairs of a B200 (workspace sizes have to be known without one)
+constexpr int kMaxSplits = 16, kMinSplitBlocks = 8;
+
+int dh_splits(const Opts& o, int64_t N, int64_t H, int64_t V) {
+  const Chunking c = chunking(o, N, V);
+  if (!o.compact || N == 0) return 1;
+  const int64_t rows = std::min<int64_t>(c.tc, N);
+  const int64_t tiles = ((rows + 255) / 256) * ((H + 255) / 256);
+  const int64_t kb = (std::min<int64_t>(c.vc, V) + BK - 1) / BK;
+  return static_cast<int>(std::max<int64_t>(
+      1, std::min({static_cast<int64_t>(kMaxSplits), kPlanPairs / tiles, kb / kMinSplitBlocks})));
+}
+
+// Rows between two splits' blocks (stores come in boxes of 32 rows).
+int64_t dh_split_rows(const Opts& o, int64_t N, int64_t V) {
+  return static_cast<int64_t>(
+      align_up(std::min<int64_t>(chunking(o, N, V).tc, std::max<int64_t>(N, 1)), 256));
+}
+
 // Backward counters of one call, zeroed at its start: a dynamic tile counter
 // for each GEMM launch (at most three per chunk), then one per chunk that the
 // CTAs of its gradient launches count themselves out on.
@@ -339,7 +363,7 @@ int64_t bwd_counters(const Opts& o, int64_t N, int64_t V) { return 4 * bwd_chunk
 // key/value buffers, digit counts) | label residuals | compact hidden [N, H]
 // bf16 | dZ block, whose space the dWeight label correction's run pieces
 // reuse once the GEMMs are done | compact-order dHidden of one token chunk
-// [chunk_tokens, H] fp32 (row compaction only).
+// [chunk_tokens, H] fp32 (row compaction only), or one block for each of dh_splits.
 struct BwdLayout {
   size_t counters, perm, labels_c, lse_c, block_valid, n_valid_c, keys0, keys1, vals0, vals1,
       hist, resid, hidden_c, gblock, gblock_bytes, part, dh_c, end;
@@ -378,7 +402,11 @@ BwdLayout bwd_layout(const Opts& o, int64_t N, int64_t H, int64_t V) {
                   nseg * 2 * static_cast<size_t>(H) * 4);
   off = align_up(off, 1024);
   L.dh_c = off;
-  if (o.compact) off += static_cast<size_t>(c.tc) * static_cast<size_t>(H) * 4;
+  if (o.compact) {
+    const int splits = dh_splits(o, N, H, V);
+    const size_t rows = splits > 1 ? splits * static_cast<size_t>(dh_split_rows(o, N, V)) : 0;
+    off += std::max(static_cast<size_t>(c.tc), rows) * static_cast<size_t>(H) * 4;
+  }
   L.end = off;
   return L;
 }
@@ -504,7 +532,8 @@ cudaError_t run_gemm_cg(DevInfo* d, int kind, const GemmProblem& p0,
   const GemmProblem& q1 = p1 ? *p1 : p0;
   // what is handed out: tiles, or runs of column tiles
   const int tiles = Epi::kRun ? g0.m_tiles * g0.runs
-                              : g0.m_tiles * g0.n_tiles + g1.m_tiles * g1.n_tiles;
+                              : g0.m_tiles * g0.n_tiles * std::max(1, g0.k_splits) +
+                                    g1.m_tiles * g1.n_tiles * std::max(1, g1.k_splits);
   const int units = std::max(1, std::min(tiles, d->sms / kCG));
   if (ctas_out != nullptr) *ctas_out = units * kCG;
   cudaLaunchConfig_t cfg = {};
@@ -773,13 +802,13 @@ flce_status forward_fp32(DevInfo* d, const void* hidden, const void* weight,
 // tiles (157 K-blocks) are four of 512 or eight of 256 columns, for 74 CTA pairs:
 // 106 or 60 us.
 int grad_tile_cols(const Opts& o, int sms, int64_t rows, int64_t cols, int64_t H, bool dh,
-                   bool dw) {
+                   bool dw, int splits) {
   if (o.grad_bn != 512) return o.grad_bn;
   const auto time = [&](int64_t bn) {
     const int64_t nt = (H + bn - 1) / bn;
     const int64_t kh = dh ? (cols + BK - 1) / BK : 0, kw = dw ? (rows + BK - 1) / BK : 0;
     const int64_t all = ((rows + 255) / 256 * kh + (cols + 255) / 256 * kw) * nt * bn;
-    return std::max(std::max(kh, kw) * bn, all / std::max(1, sms / 2));
+    return std::max(std::max((kh + splits - 1) / splits, kw) * bn, all / std::max(1, sms / 2));
   };
   return 4 * time(512) > 5 * time(256) ? 256 : 512;
 }
@@ -900,7 +929,9 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
   // else d_hidden itself.
   float* dh_c = compact ? reinterpret_cast<float*>(w + BL.dh_c) : nullptr;
   float* dh_out = compact ? dh_c : d_hidden;
-  const int64_t dh_rows = compact ? ck.tc : N;
+  const int splits = rg != nullptr ? dh_splits(o, N, H, V) : 1;
+  const int64_t split_rows = dh_split_rows(o, N, V);
+  const int64_t dh_rows = splits > 1 ? splits * split_rows : (compact ? ck.tc : N);
   CUtensorMap t_hid_k, t_hid_mn, t_w_k, t_w_mn, t_dh, t_dw;
   if (!make_map(&t_hid_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, hid, H, N, H * 2, BK, BM) ||
       !make_map(&t_hid_mn, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, hid, H, N, H * 2, 64, BK) ||
@@ -1022,6 +1053,8 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
       gh.rows_dim = kRowsM;
       gh.dep_wait = kDepBeforeLoads;  // reads the dZ block written just before
       gh.b_mn3d = h3d ? 1 : 0;
+      gh.k_splits = splits;
+      gh.split_rows = static_cast<int>(split_rows);
       if (o.dz_buffers > 1) gh.done_counter = done + ci;
       const bool last_v = v0 + ck.vc >= V;
       StoreEpi::Params eh{compact ? 0 : static_cast<int>(t0),
@@ -1052,7 +1085,7 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
 
       const GemmProblem ph{&t_g_k, &t_w_mn, &t_dh, rows, H, gh};
       const GemmProblem pw{&t_g_mn, &t_hid_mn, &t_dw, cols, H, gw};
-      const int gbn = grad_tile_cols(o, d->sms, rows, cols, H, want_dh, want_dw);
+      const int gbn = grad_tile_cols(o, d->sms, rows, cols, H, want_dh, want_dw, splits);
       int ctas = 0;
       if (want_dh && want_dw && o.fuse) {
         // 2) + 3) in one launch: the dWeight tiles fill the dHidden grid's last wave
@@ -1079,7 +1112,8 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
               reinterpret_cast<const float4*>(dh_c), static_cast<int>(t0), rows, perm,
               rows_valid, lab, resid, static_cast<const __nv_bfloat16*>(weight), V,
               static_cast<int>(H / 4), reinterpret_cast<float4*>(d_hidden), acc_dh ? 1 : 0,
-              grad_output, grad_scale, n_valid, mean);
+              grad_output, grad_scale, n_valid, mean, splits,
+              static_cast<size_t>(split_rows) * (static_cast<size_t>(H) / 4));
         });
         if (e != cudaSuccess) return cuda_fail(e);
       }

@@ -100,6 +100,7 @@ constexpr int kMaxTopCap = top_list_cap(kMaxTopList);
 template <bool kSoftcap>
 struct ScoreEpi {
   static constexpr bool kRun = true;
+  static constexpr bool kSplit = false;
   static constexpr int kEpiWarps = 8;
   static constexpr int kStagingPerWarp = 32 * 32 * 4;  // 32 columns of 32 rows (see scan)
   __device__ static void init_smem(uint8_t*) {}
@@ -315,7 +316,7 @@ struct ScoreEpi {
   __device__ static bool tile(const Params& p, const Pre& pre, int m_base, int col0,
                               uint32_t taddr, int q, int lane, int part, uint8_t* stg,
                               const CUtensorMap*, uint32_t tempty, State& S, bool,
-                              const volatile int*, unsigned long long) {
+                              const volatile int*, unsigned long long, int) {
     if (col0 >= p.V) {  // the second bank of a 512-column tile past the vocabulary
       release_tmem(tempty, lane);
       return true;
@@ -575,7 +576,7 @@ struct FinishArgs {
 __device__ __forceinline__ double dot_part(const __nv_bfloat16* a, const __nv_bfloat16* b, int H,
                                            int lane) {
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
+#pragma unroll 8
   for (int k = lane * 8; k < H; k += 256) {  // H is a multiple of 8
     const uint4 x = *reinterpret_cast<const uint4*>(a + k);
     const uint4 y = __ldg(reinterpret_cast<const uint4*>(b + k));

@@ -561,14 +561,16 @@ __global__ void __launch_bounds__(256)
 // (fp32, chunk-local rows, TMA store then reduce-add); here compact row j
 // adds the exact label term g * resid[j] * W[labels_c[j]] and lands on
 // d_hidden row perm[j] (stored, or added with `accumulate`).  Rows past the
-// valid count are not read: the GEMMs skip or leave them undefined.
+// valid count are not read: the GEMMs skip or leave them undefined.  With
+// splits > 1 the row is the sum, in order, of as many blocks split_stride apart.
 __global__ void __launch_bounds__(256)
     dh_scatter_kernel(const float4* __restrict__ dh_c, int t0, int rows,
                       const int* __restrict__ perm, const long long* __restrict__ n_valid,
                       const int64_t* __restrict__ labels_c, const float* __restrict__ resid,
                       const __nv_bfloat16* __restrict__ weight, int64_t V, int H4,
                       float4* __restrict__ d_hidden, int accumulate, const float* grad_output,
-                      float grad_scale, const long long* n_valid_for_mean, int mean) {
+                      float grad_scale, const long long* n_valid_for_mean, int mean, int splits,
+                      size_t split_stride) {
   const int jl = blockIdx.x;
   const long long j = static_cast<long long>(t0) + jl;
   if (jl >= rows || j >= *n_valid) return;
@@ -581,6 +583,13 @@ __global__ void __launch_bounds__(256)
   const uint2* wrow = reinterpret_cast<const uint2*>(weight + static_cast<size_t>(fix ? y : 0) * H4 * 4);
   for (int k = threadIdx.x; k < H4; k += blockDim.x) {
     float4 o = src[k];
+    for (int sp = 1; sp < splits; ++sp) {
+      const float4 more = src[sp * split_stride + k];
+      o.x += more.x;
+      o.y += more.y;
+      o.z += more.z;
+      o.w += more.w;
+    }
     if (fix) {
       const uint2 wv = wrow[k];
       const float2 w01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wv.x));

@@ -165,6 +165,10 @@ struct GemmArgs {
   // handed out in runs of consecutive column tiles of one row tile, `runs` per
   // row tile, cut as RunMap{run_n, run_c0, run_q} says.
   int run_n, run_c0, run_q, runs;
+  // Epilogues with kSplit: the K-blocks are cut into k_splits ranges (0 or 1: one),
+  // each a tile of its own; range s of a tile goes to output rows s * split_rows
+  // further down, for a later kernel to add in order.
+  int k_splits, split_rows;
 };
 
 constexpr int kRowsNone = 0;
@@ -217,6 +221,22 @@ struct RunMap {
     return run + tile / len;
   }
 };
+
+// The split of virtual row tile mb, and its K-blocks [kb0, kb0 + count); mb becomes the
+// row tile's own index.
+__device__ __forceinline__ int split_range(const GemmArgs& g, int& mb, int& kb0, int& count) {
+  if (g.k_splits <= 1) {
+    kb0 = 0;
+    count = g.k_blocks;
+    return 0;
+  }
+  const int rows = g.m_tiles / g.k_splits, s = mb / rows;
+  mb -= s * rows;
+  const int per = (g.k_blocks + g.k_splits - 1) / g.k_splits;
+  kb0 = min(s * per, g.k_blocks);
+  count = min(per, g.k_blocks - kb0);
+  return s;
+}
 
 // tile_coords for runs: tile index = run_n * (run in raster order) + position in
 // the run; `left` receives the tiles from here to the run's end.
@@ -282,6 +302,7 @@ template <bool kSoftcap>
 struct FwdStatsEpi {
   using State = int;  // banks seen by this warp
   static constexpr bool kRun = false;
+  static constexpr bool kSplit = false;
   static constexpr int kEpiWarps = 8;
   // first warp of a quadrant: its mbarriers full[2], empty[2]; second warp:
   // the two (m[32], s[32]) slots
@@ -315,7 +336,7 @@ struct FwdStatsEpi {
   __device__ static bool tile(const Params& p, const Pre& pre, int m_base, int col0,
                               uint32_t taddr, int q, int lane, int part, uint8_t* stg,
                               const CUtensorMap*, uint32_t tempty, int& nbank, bool,
-                              const volatile int* abort, unsigned long long timeout_ns) {
+                              const volatile int* abort, unsigned long long timeout_ns, int) {
     if (col0 >= p.V) {  // the second bank of a 512-column tile past the vocabulary
       release_tmem(tempty, lane);
       return true;
@@ -479,6 +500,7 @@ template <bool kSoftcap, bool kRowGrads = false>
 struct DzEpi {
   using State = int;  // TMA stores issued by this warp
   static constexpr bool kRun = false;
+  static constexpr bool kSplit = false;
   // Eight warps: the two warps of a TMEM lane quadrant each take 128 of a
   // bank's columns.  One 4 KiB staging buffer per warp (32 rows x 64 bf16).
   static constexpr int kEpiWarps = 8;
@@ -531,7 +553,7 @@ struct DzEpi {
   __device__ static bool tile(const Params& p, const Pre& pre, int m_base, int col0,
                               uint32_t taddr, int q, int lane, int part, uint8_t* stg,
                               const CUtensorMap* out, uint32_t tempty, int& nstore, bool,
-                              const volatile int*, unsigned long long) {
+                              const volatile int*, unsigned long long, int) {
     // this warp's columns: [h0, h0 + 128) of the block; 64-column stores whose
     // box starts inside the block (warp-uniform)
     const int h0 = col0 + part * (BN / 2);
@@ -689,6 +711,7 @@ struct DzEpi {
 struct StoreEpi {
   using State = int;  // TMA stores issued by this warp
   static constexpr bool kRun = false;
+  static constexpr bool kSplit = true;
   // Eight warps: the two warps of a TMEM lane quadrant each take 128 of a
   // bank's columns.  One 4 KiB staging buffer per warp (32 rows x 32 fp32).
   static constexpr int kEpiWarps = 8;
@@ -698,7 +721,7 @@ struct StoreEpi {
     int out_row0;
     int reduce;
     int x_limit;  // output columns
-    int y_limit;  // output rows
+    int y_limit;  // output rows (of one split)
     const float* grad_output;  // may be null (1.0)
     float grad_scale;
     const long long* n_valid;  // device count of non-ignored rows
@@ -723,13 +746,13 @@ struct StoreEpi {
   __device__ static bool tile(const Params& p, const Pre& pre, int m_base, int col0,
                               uint32_t taddr, int q, int lane, int part, uint8_t* stg,
                               const CUtensorMap* out, uint32_t tempty, int& nstore,
-                              bool empty, const volatile int*, unsigned long long) {
+                              bool empty, const volatile int*, unsigned long long, int split_row) {
     // this warp's columns: [h0, h0 + 128); 32-column stores whose box starts
     // inside the output (warp-uniform)
     const int h0 = col0 + part * (BN / 2);
-    const int y = p.out_row0 + m_base + q * 32;
+    const int y_own = p.out_row0 + m_base + q * 32, y = y_own + split_row;
     const int rem = p.x_limit - h0;
-    const int nch = (y >= p.y_limit || rem <= 0) ? 0 : min(BN / 2 / 32, (rem + 31) / 32);
+    const int nch = (y_own >= p.y_limit || rem <= 0) ? 0 : min(BN / 2 / 32, (rem + 31) / 32);
     if (nch == 0) {
       release_tmem(tempty, lane);
       return true;
@@ -902,6 +925,9 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
         if (g.k_blocks == 0 && !g.zero_if_empty) g.m_tiles = 0;
       }
     }
+    if constexpr (Epi::kSplit) {
+      if (g.k_splits > 1) g.m_tiles *= g.k_splits;
+    }
     return g;
   };
   const GemmArgs a0 = bound_rows(g0);
@@ -1012,6 +1038,8 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
         int prob, mb, nb;
         locate(tile, prob, mb, nb);
         const GemmArgs& g = prob ? a1 : a0;
+        int kb0 = 0, kbn = g.k_blocks;
+        if constexpr (Epi::kSplit) split_range(g, mb, kb0, kbn);
         const CUtensorMap* mA = prob ? &tmA1 : &tmA0;
         const CUtensorMap* mB = prob ? &tmB1 : &tmB0;
         const bool a_mn = prob ? kAMn1 : kAMn0;
@@ -1019,7 +1047,7 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
         const int m_cta = mb * Cfg::kUnitRows + static_cast<int>(rank) * BM;
         // bank h of the tile: B rows nb * kBN + h * BN + [rank * kBankRows, + kBankRows)
         const int n_cta = nb * kBN + static_cast<int>(rank) * Cfg::kBankRows;
-        for (int kb = 0; kb < g.k_blocks; ++kb) {
+        for (int kb = kb0; kb < kb0 + kbn; ++kb) {
           if (!mbar_wait(smem_u32(&bar_empty[stage]), phase ^ 1u, abort_flag, g0.timeout_ns)) {
             ok = false;
             break;
@@ -1121,7 +1149,12 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
         }
         if (!ok || tile >= num_tiles) break;
         const int prob = (tile < tiles0) ? 0 : 1;
-        const int k_blocks = prob ? a1.k_blocks : a0.k_blocks;
+        int k_blocks = prob ? a1.k_blocks : a0.k_blocks;
+        if constexpr (Epi::kSplit) {
+          int p, mb, nb, kb0;
+          locate(tile, p, mb, nb);
+          split_range(prob ? a1 : a0, mb, kb0, k_blocks);
+        }
         const uint32_t idesc = prob ? idesc1 : idesc0;
         const bool a_mn = prob ? kAMn1 : kAMn0;
         const bool b_mn = prob ? kBMn1 : kBMn0;
@@ -1248,8 +1281,10 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
       if (!ok || tile >= num_tiles) break;
       int prob, mb, nb;
       locate(tile, prob, mb, nb);
-      const int m_base = mb * Cfg::kUnitRows + static_cast<int>(rank) * BM;
       const GemmArgs& ga = prob ? a1 : a0;
+      int split = 0, kb0 = 0, kbn = ga.k_blocks;
+      if constexpr (Epi::kSplit) split = split_range(ga, mb, kb0, kbn);
+      const int m_base = mb * Cfg::kUnitRows + static_cast<int>(rank) * BM;
       // per-row inputs of the epilogue, in flight while the MMAs finish
       const typename Epi::Pre pre = Epi::prepare(prob ? ep1 : ep0, m_base, q, lane);
       // the tile's first bank and the phase its full barrier completes
@@ -1269,8 +1304,8 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
         const uint32_t tempty_local = smem_u32(&bar_tempty[bank]);
         const uint32_t tempty = (kCG == 1) ? tempty_local : mapa_shared(tempty_local, 0);
         if (!Epi::tile(prob ? ep1 : ep0, pre, m_base, nb * kBN + h * BN, taddr, q, lane, part,
-                       stg, prob ? &tmOut1 : &tmOut0, tempty, state, ga.k_blocks == 0,
-                       abort_flag, g0.timeout_ns)) {
+                       stg, prob ? &tmOut1 : &tmOut0, tempty, state, kbn == 0, abort_flag,
+                       g0.timeout_ns, split * ga.split_rows)) {
           ok = false;
           break;
         }

@@ -440,3 +440,28 @@ def test_refusals_on_the_device():
         flce.logprobs_backward(h, w, y, f.saved, torch.ones(4, device="cuda"))
     with pytest.raises(ValueError):
         flce.logprobs_backward(h, w, y, f.lse, f.lse)
+
+
+@pytest.mark.parametrize("N,H,V", [(1, 64, 5000), (40, 128, 3000), (300, 72, 9000),
+                                   (257, 264, 2100)])
+def test_backward_of_few_tokens_cuts_the_vocabulary(N, H, V):
+    """Few token rows: dHidden's sum over the vocabulary runs in several ranges that
+    are added in order, over one and over several chunks."""
+    host, dev = problem(N, H, V, seed=N + V, n_ign=N // 5)
+    a = np.random.default_rng(26).standard_normal(N).astype(np.float32)
+    f = flce.logprobs_forward(*dev)
+    up = torch.from_numpy(a).cuda()
+    rh, rw = ref.backward(*host, a, None, IGN)
+    t_h, t_w = gradient_tolerance(host[0], host[1], ref.dz(*host, a, None, IGN), host[2])
+    for tokens, vocab in ((16384, 16384), (256, 1280)):
+        with G.chunks(tokens, vocab):
+            first = flce.logprobs_backward(*dev, f.saved, up, check_status=True)
+            again = flce.logprobs_backward(*dev, f.saved, up)
+            base = torch.randn_like(first[0])
+            acc, _ = flce.logprobs_backward(*dev, f.saved, up, d_hidden=base.clone(),
+                                            accumulate_d_hidden=True, compute_d_weight=False)
+        for x, y, r, t in zip(first, again, (rh, rw), (t_h, t_w)):
+            assert torch.equal(x, y)
+            assert G.rel_l2(x.cpu().numpy(), r) <= t
+        # two fp32 roundings of sums of at most about 8
+        assert (acc - (base + first[0])).abs().max() <= 1e-5
