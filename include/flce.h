@@ -259,10 +259,12 @@ flce_status flce_backward_ex(const void* hidden, const void* weight, const int64
  *
  * A row whose token is ignore_index takes no part: logprobs, entropy, lse and
  * top_logprobs 0, top_ids -1.  A token outside [0, V) is reported as
- * FLCE_ERR_LABEL_RANGE and its row treated the same way.  Logits of -inf are
- * probabilities of 0 (they add nothing to the entropy and are never
- * alternatives); where fewer than top_k logits lie above -inf the places left
- * hold id -1 and log probability -inf.  A NaN or +inf logit makes
+ * FLCE_ERR_LABEL_RANGE and its row treated the same way.  Raw logits (Z) at or
+ * below -1e30, as masks of -inf or of the type's lowest value give, are never
+ * alternatives, and without softcap they are probabilities of 0 that add nothing
+ * to lse or entropy and have log probability -inf; where fewer than top_k lie
+ * above, the places left hold id -1 and log probability -inf.  A row with nothing
+ * above has lse -inf, and log probability and entropy NaN.  A NaN or +inf logit makes
  * lse, entropy and log probabilities of its row NaN (which ids a row with a NaN
  * logit lists is not defined). */
 

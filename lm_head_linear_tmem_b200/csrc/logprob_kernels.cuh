@@ -22,8 +22,9 @@ constexpr int kMaxTopK = 32;
 constexpr int kTopMargin = 4;
 constexpr int kMaxTopList = kMaxTopK + kTopMargin;
 
-// A running maximum that nothing has been merged into.  Finite, so that the
-// differences of two maxima are never inf - inf.
+// Logits at or below this count as -inf: masked columns, whether a mask wrote -inf or
+// the type's lowest value.  Also the running maximum that nothing has been merged
+// into (in log2 units): finite, so that the difference of two maxima is never inf - inf.
 constexpr float kNoMax = -1e30f;
 
 // Order-preserving map of the floats (no NaN) onto unsigned; 0 lies below all.
@@ -65,7 +66,7 @@ __device__ __forceinline__ void stats_merge(Stats& a, Stats b) {
 }
 
 // One entry of a list of large logits: the logit before softcap and temperature
-// (both keep the order; > -inf) and its vocabulary id.
+// (both keep the order; > kNoMax) and its vocabulary id.
 struct TopEntry {
   float v;
   int id;
@@ -330,7 +331,7 @@ struct ScoreEpi {
     if (first) {
       S.st = Stats{kNoMax, 0.f, 0.f};
       S.zmax = -CUDART_INF_F;
-      S.above = row_ok ? -CUDART_INF_F : CUDART_INF_F;  // rows past the end take nothing
+      S.above = row_ok ? kNoMax : CUDART_INF_F;  // rows past the end take nothing
       S.n = 0;
     }
     const size_t at = static_cast<size_t>(row) * p.slots + run * 2 + part;
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kScoreThreads)
     int n = 0;
     float top = -CUDART_INF_F;
     for (; n < K; ++n) {
-      float best = -CUDART_INF_F;
+      float best = kNoMax;
       int id = -1;
       for (int c = lane; c < cols; c += 32)
         if (z[c] > best) {
@@ -800,7 +801,8 @@ __global__ void __launch_bounds__(kFinishThreads)
   double x = 0.0;
   if (t <= a.K) {
     const double z = zx[t];
-    x = (a.softcap > 0.f ? a.softcap * tanh(z / a.softcap) : z) * a.inv_temp;
+    x = (a.softcap > 0.f ? a.softcap * tanh(z / a.softcap)
+                         : (z <= kNoMax ? -CUDART_INF : z)) * a.inv_temp;
     xe[t] = x;
   }
   __syncthreads();
@@ -889,7 +891,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     }
     if (rank < a.top_k) {
       a.top_logprobs[static_cast<size_t>(row) * a.top_k + rank] =
-          static_cast<float>(x - lse_sh);
+          id < 0 ? -CUDART_INF_F : static_cast<float>(x - lse_sh);
       a.top_ids[static_cast<size_t>(row) * a.top_k + rank] = id;
     }
   }

@@ -43,7 +43,7 @@ def embedding_forward(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.
     y = _ids(ids, dev)
     w = weight.contiguous()
     V, H = w.shape
-    out = torch.empty((y.shape[0], H), dtype=w.dtype, device=dev)
+    out = torch.empty(ids.shape + (H,), dtype=w.dtype, device=dev)
     word = torch.empty(1, dtype=torch.int32, device=dev) if check_status else None
     with on_device(dev):
         st = _lib().flce_embedding_forward(_ptr(w), _ptr(y), y.shape[0], H, V, int(ignore_index),
@@ -52,7 +52,7 @@ def embedding_forward(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.
     _native.check(st, "flce_embedding_forward")
     if check_status and int(word) != 0:
         raise _native.FlceError(_native.LABEL_RANGE, "flce_embedding_forward (device status)")
-    return out if ids.dim() == 1 else out.view(*ids.shape, H)
+    return out
 
 
 def embedding_workspace_bytes(N: int, H: int, V: int) -> int:

@@ -63,26 +63,25 @@ def logprobs_forward(hidden: torch.Tensor, weight: torch.Tensor,
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     else:
         check_workspace(workspace, dev)
-    # one allocation for the float outputs of a row: saved (2), entropy, lse, logprobs
-    f = torch.empty((4 if y is None else 5, N), dtype=torch.float32, device=dev)
-    at = f.data_ptr()
-    top_lp = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
-    top_ids = torch.empty((N, k), dtype=torch.int64, device=dev) if k else None
+    # outputs of their own (not views of one buffer: a caller may change them in place)
+    def rows(*more, dtype=torch.float32):
+        return torch.empty(lead + more, dtype=dtype, device=dev)
+
+    saved = torch.empty((2, N), dtype=torch.float32, device=dev)
+    logprobs = None if y is None else rows()
+    entropy, lse = rows(), rows()
+    top_lp = rows(k) if k else None
+    top_ids = rows(k, dtype=torch.int64) if k else None
     with on_device(dev):
         st = _lib().flce_logprobs_forward(
             _ptr(h2), _ptr(w), _ptr(y), N, H, V, int(ignore_index), float(softcap),
-            float(temperature), k, _DTYPES[h2.dtype], None if y is None else at + 16 * N,
-            at + 8 * N, at + 12 * N, at, _ptr(top_lp), _ptr(top_ids), _ptr(workspace),
-            workspace.numel(), _stream(dev))
+            float(temperature), k, _DTYPES[h2.dtype], _ptr(logprobs), _ptr(entropy), _ptr(lse),
+            _ptr(saved), _ptr(top_lp), _ptr(top_ids), _ptr(workspace), workspace.numel(),
+            _stream(dev))
     _native.check(st, "flce_logprobs_forward")
     if check_status:
         _native.check(status(workspace), "flce_logprobs_forward (device status)")
-    rows = f[2:].unbind(0)
-    if len(lead) != 1:
-        rows = [t.view(lead) for t in rows]
-        if k:
-            top_lp, top_ids = top_lp.view(*lead, k), top_ids.view(*lead, k)
-    return Logprobs(None if y is None else rows[2], rows[0], rows[1], top_lp, top_ids, f[:2])
+    return Logprobs(logprobs, entropy, lse, top_lp, top_ids, saved)
 
 
 def _row_grad(t: Optional[torch.Tensor], name: str, N: int, dev) -> Optional[torch.Tensor]:

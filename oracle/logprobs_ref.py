@@ -8,9 +8,11 @@ import numpy as np
 
 
 def logits(hidden, weight, softcap=0.0, temperature=1.0):
-    """(z, x): the raw logits and those that the softmax sees, float64 [N, V]."""
+    """(z, x): the raw logits and those that the softmax sees, float64 [N, V]; raw
+    logits at or below -1e30 (masks) count as -inf."""
     with np.errstate(invalid="ignore", over="ignore"):
         z = np.asarray(hidden, np.float64) @ np.asarray(weight, np.float64).T
+        z = np.where(z <= -1e30, -np.inf, z)
         x = softcap * np.tanh(z / softcap) if softcap > 0 else z
         return z, x / temperature
 

@@ -175,7 +175,7 @@ def test_alternatives_in_unfavourable_orders(N, order):
 @pytest.mark.parametrize("low", [-np.inf, -3.3895313892515355e38])
 def test_columns_switched_off_by_their_weight(N, low, dtype):
     """A logit of -inf, or of the type's lowest value, is a probability of zero:
-    nothing of it reaches the entropy, and -inf is never an alternative."""
+    nothing of it reaches the entropy, and it is never an alternative."""
     g = np.random.default_rng(7)
     h = np.zeros((N, 8), np.float32)
     h[:, 0] = 1.0
@@ -194,10 +194,44 @@ def test_columns_switched_off_by_their_weight(N, low, dtype):
     assert np.abs(got.entropy.cpu().numpy() - f["entropy"]).max() < 1e-5
     ids = got.top_ids.cpu().numpy()
     assert np.array_equal(ids[:, :4], f["top_ids"][:, :4])
+    assert np.all(ids[:, 4:] == -1) and np.all(np.isneginf(got.top_logprobs.cpu()[:, 4:].numpy()))
+    # a token that is masked has probability 0
+    off_tok = torch.full((N,), 6, device="cuda")
+    assert torch.isneginf(flce.logprobs_forward(dev[0], dev[1], off_tok).logprobs).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [6, 200])
+@pytest.mark.parametrize("low", [-np.inf, -3.3895313892515355e38])
+def test_rows_whose_mask_leaves_nothing(N, low, dtype):
+    """Row 2 sees only masked columns: no alternatives, nothing to take a logarithm
+    of; the other rows are as without it."""
+    g = np.random.default_rng(27)
+    h = np.zeros((N, 8), np.float32)
+    h[:, 1:] = g.integers(1, 3, (N, 7))
+    w = np.zeros((300, 8), np.float32)
+    w[:, 1:] = g.integers(-2, 3, (300, 7))
+    host, dev = on_gpu(h, w, np.full(N, 5), dtype)
+    clean = flce.logprobs_forward(*dev, top_k=4)
+    wide = dev[1].clone()
+    wide[:, 0] = low
+    hid = dev[0].clone()
+    # finite weights (or zero hidden entries against -inf would be NaN)
     if np.isinf(low):
-        assert np.all(ids[:, 4:] == -1) and np.all(np.isneginf(got.top_logprobs.cpu()[:, 4:].numpy()))
+        hid = hid[2:3].clone()
+        hid[:, 0] = 1.0
+        got = flce.logprobs_forward(hid, wide, dev[2][2:3], top_k=4, check_status=True)
+        row = 0
     else:
-        assert np.array_equal(ids, f["top_ids"])
+        hid[2, 0] = 1.0
+        got = flce.logprobs_forward(hid, wide, dev[2], top_k=4, check_status=True)
+        row = 2
+        keep = [i for i in range(N) if i != 2]
+        for a, b in zip(clean[:5], got[:5]):
+            assert torch.equal(a[keep], b[keep])
+    assert torch.all(got.top_ids[row] == -1) and torch.isneginf(got.top_logprobs[row]).all()
+    assert torch.isneginf(got.lse[row])
+    assert torch.isnan(got.logprobs[row]) and torch.isnan(got.entropy[row])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
@@ -333,6 +367,40 @@ def test_autograd_shapes_and_broadcast_gradients():
     t_h, t_w = gradient_tolerance(host[0], host[1], ref.dz(*host, a, b, IGN, 0.0, 0.9), host[2])
     assert G.rel_l2(h.grad.float().cpu().numpy().reshape(140, 64), rh) <= t_h + 2.0 ** -8
     assert G.rel_l2(w.grad.float().cpu().numpy(), rw) <= t_w + 2.0 ** -8
+
+
+def test_results_may_be_changed_in_place():
+    _, dev = problem(2 * 30, 64, 500, seed=28)
+    h = dev[0].view(2, 30, 64).requires_grad_()
+    f = flce.fused_linear_logprobs(h, dev[1], dev[2].view(2, 30), top_k=2)
+    want, = torch.autograd.grad((3.0 * f.logprobs).sum(), h, retain_graph=True)
+    f.logprobs.mul_(3.0)
+    f.lse.zero_()
+    f.top_logprobs.zero_()
+    got, = torch.autograd.grad(f.logprobs.sum(), h)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("opt", [{"bwd_compact": 0}, {"cta_group": 1}, {"bwd_fuse": 0},
+                                 {"dz_buffers": 2}, {"mn3d": 0}, {"grad_tile_n": 256},
+                                 {"dz_tile_n": 256}, {"bwd_compact": 0, "cta_group": 1}])
+@pytest.mark.parametrize("softcap", [0.0, 4.0])
+def test_every_backward_schedule(opt, softcap):
+    host, dev = problem(600, 136, 3000, seed=29, n_ign=100)
+    g = np.random.default_rng(30)
+    a, b = (g.standard_normal(600).astype(np.float32) for _ in range(2))
+    up = [torch.from_numpy(t).cuda() for t in (a, b)]
+    rh, rw = ref.backward(*host, a, b, IGN, softcap, 0.8)
+    d = ref.dz(*host, a, b, IGN, softcap, 0.8)
+    # without the compaction there is no fp32 label correction: label entries round too
+    y = np.full(600, IGN) if "bwd_compact" in opt else host[2]
+    t_h, t_w = gradient_tolerance(host[0], host[1], d, y)
+    f = flce.logprobs_forward(*dev, softcap=softcap, temperature=0.8)
+    with _native.options(chunk_tokens=256, chunk_vocab=1024, **opt):
+        dh, dw = flce.logprobs_backward(*dev, f.saved, *up, softcap=softcap, temperature=0.8,
+                                        check_status=True)
+    assert G.rel_l2(dh.cpu().numpy(), rh) <= t_h
+    assert G.rel_l2(dw.cpu().numpy(), rw) <= t_w
 
 
 def test_entropy_alone_needs_no_tokens():
