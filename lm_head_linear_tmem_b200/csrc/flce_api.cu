@@ -55,6 +55,8 @@ constexpr int kGroupM = 16;     // forward and dZ
 constexpr int kGroupMGrad = 8;  // dHidden and dWeight: their long-K panels (8 MiB at the bench
                                 // size) make a 16-tile group's panels overflow L2 (ncu: 2.4 vs
                                 // 2.8 GB of DRAM reads per launch)
+constexpr int kPlanSms = 148;   // SMs of a B200, where a plan decides workspace sizes (which have to
+                                // be known without a device)
 constexpr size_t kHeaderBytes = 256;
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1024;
 constexpr int kSimtMaxH = 12288;
@@ -334,7 +336,6 @@ int64_t bwd_chunks(const Opts& o, int64_t N, int64_t V) {
 // in order: where the token rows make too few tiles for the SMs, the time would be that of one
 // tile's K loop over the whole vocabulary chunk.  1: not cut.
 // 400 x 1000 x 10007 (8 tiles of 157 K-blocks): the launch took 71 us uncut.
-constexpr int kPlanPairs = 74;  // CTA pairs of a B200 (workspace sizes have to be known without one)
 constexpr int kMaxSplits = 16, kMinSplitBlocks = 8;
 
 int dh_splits(const Opts& o, int64_t N, int64_t H, int64_t V) {
@@ -344,7 +345,7 @@ int dh_splits(const Opts& o, int64_t N, int64_t H, int64_t V) {
   const int64_t tiles = ((rows + 255) / 256) * ((H + 255) / 256);
   const int64_t kb = (std::min<int64_t>(c.vc, V) + BK - 1) / BK;
   return static_cast<int>(std::max<int64_t>(
-      1, std::min({static_cast<int64_t>(kMaxSplits), kPlanPairs / tiles, kb / kMinSplitBlocks})));
+      1, std::min({static_cast<int64_t>(kMaxSplits), kPlanSms / 2 / tiles, kb / kMinSplitBlocks})));
 }
 
 // Rows between two splits' blocks (stores come in boxes of 32 rows).

@@ -3,7 +3,7 @@
 // distribution softmax(x), x = softcap(hidden . weight^T) / temperature.
 //
 //   ScoreEpi        epilogue of the tcgen05 GEMM (tc_gemm.cuh): streaming softmax
-//                   statistics and a sorted list of the largest logits per row
+//                   statistics and the candidates for the largest logits of a row
 //   score_simt      the same partial results for float32 inputs (CUDA cores)
 //   score_finish    joins a row's partial results and evaluates the outputs
 #pragma once
@@ -167,7 +167,8 @@ struct ScoreEpi {
   template <int n, class F>
   __device__ static float kth_largest(const F& value, int K, float mx) {
     uint32_t lo = order_key(-CUDART_INF_F), hi = order_key(mx);
-    while (__any_sync(0xffffffffu, lo < hi)) {
+    // (32 halvings settle any interval)
+    for (int it = 0; it < 32 && __any_sync(0xffffffffu, lo < hi); ++it) {
       const uint32_t mid = lo + (hi - lo + 1u) / 2u;
       if (at_least<n>(value, order_value(mid)) >= K)
         lo = mid;
@@ -182,10 +183,14 @@ struct ScoreEpi {
   // maxima, which about nine columns reach, goes down in growing steps while
   // fewer than K reach it, and then halves; the second largest maximum is the
   // upper end, so that one logit far above the others does not stretch the range.
-  __device__ static float near_kth(const uint32_t (&r)[4][32], int K, const float (&mx)[4]) {
+  __device__ static float near_kth(const uint32_t (&r)[4][32], int K, const float (&mx)[4],
+                                   float mx_all) {
     const auto value = [&](int j) { return __uint_as_float(r[j / 32][j % 32]); };
-    const float a0 = fminf(mx[0], mx[1]), a1 = fmaxf(mx[0], mx[1]);
-    const float b0 = fminf(mx[2], mx[3]), b1 = fmaxf(mx[2], mx[3]);
+    float m[4];  // a chunk past the vocabulary, or masked, says nothing
+#pragma unroll
+    for (int c = 0; c < 4; ++c) m[c] = mx[c] <= kNoMax ? mx_all : mx[c];
+    const float a0 = fminf(m[0], m[1]), a1 = fmaxf(m[0], m[1]);
+    const float b0 = fminf(m[2], m[3]), b1 = fmaxf(m[2], m[3]);
     float hi = fmaxf(fminf(a1, b1), fmaxf(a0, b0)), x = fminf(a0, b0);
     float step = hi - x, bound = -CUDART_INF_F;
 #pragma unroll 1
@@ -225,7 +230,7 @@ struct ScoreEpi {
     if (__any_sync(0xffffffffu, n > 2 * K + 4)) {
       // a run's start, before any CTA has seen enough of the row (or logits that
       // rise with the id): all but the block's own best would be for nothing
-      kth = near_kth(r, K, mx);
+      kth = near_kth(r, K, mx, mx_all);
       n = find(fmaxf(S.above, nextbelow(kth)));
     }
     const bool full = n > top_list_cap(K) - S.n;

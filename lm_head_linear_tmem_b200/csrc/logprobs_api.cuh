@@ -10,8 +10,6 @@
 namespace flce {
 namespace {
 
-// The plan has to be known without a device (workspace sizes): SMs of a B200.
-constexpr int kPlanSms = 148;
 // A token batch of at most one 128-row tile reads the weight once whatever the
 // tile shape; single CTAs then spend half the tensor-core time of a pair on
 // the tile's empty rows.
