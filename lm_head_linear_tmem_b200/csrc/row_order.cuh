@@ -77,6 +77,25 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem, con
     }
   }
   atomicAdd(&live_sum, live);
+  if (a.N <= kSortThreads) {
+    // few enough to count, for each token, those before it (a broadcast of four keys at
+    // a time): one step where the digits take two to four
+    __syncthreads();
+    for (int i = a.N + t; i < (a.N + 3) / 4 * 4; i += kSortThreads) key[0][i] = 0xffffffffu;
+    __syncthreads();
+    if (t < a.N) {
+      const uint32_t k = key[0][t];
+      int rank = 0;
+      for (int i = 0; i < a.N; i += 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(key[0] + i);
+        rank += (q.x < k || (q.x == k && i < t)) + (q.y < k || (q.y == k && i + 1 < t)) +
+                (q.z < k || (q.z == k && i + 2 < t)) + (q.w < k || (q.w == k && i + 3 < t));
+      }
+      put(rank, k, t, live_sum);
+    }
+    if (t == 0) *a.n_valid = live_sum;
+    return;
+  }
   const int digits = 1 << a.digit_bits, mask = digits - 1;
   for (int ps = 0; ps < a.passes; ++ps) {
     const int src = ps & 1, shift = ps * a.digit_bits;
