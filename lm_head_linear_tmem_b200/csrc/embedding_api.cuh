@@ -23,13 +23,14 @@ bool embed_sizes_ok(int64_t N, int64_t H, int64_t V) {
   return N >= 0 && V >= 1 && H >= 1 && N <= kMaxDim && V <= kMaxDim && H <= (1 << 20);
 }
 
-// Workspace: header (status word, number of joins at 4) | sorted ids and tokens, live count | pieces of runs | and, for
+// Workspace: header (status word, number of joins at 4) | sorted ids and tokens, live
+// count | joins | touched rows | pieces of runs | and, for
 // more tokens than one block sorts, the label sort's arrays.
 struct EmbedLayout {
-  size_t keys, vals, n_valid, joins, part, keys1, vals1, perm, labels_c, block_valid, hist, end;
+  size_t keys, vals, n_valid, joins, touched, part, keys1, vals1, perm, labels_c, block_valid, hist, end;
 };
 
-EmbedLayout embed_layout(int64_t N, int64_t H) {
+EmbedLayout embed_layout(int64_t N, int64_t H, int64_t V) {
   EmbedLayout L{};
   const size_t n = static_cast<size_t>(N);
   size_t off = kHeaderBytes;
@@ -42,6 +43,7 @@ EmbedLayout embed_layout(int64_t N, int64_t H) {
   L.vals = take(4 * n);
   L.n_valid = take(8);
   L.joins = take(4 * ((n + kEmbedSeg - 1) / kEmbedSeg));
+  L.touched = take(4 * ((static_cast<size_t>(V) + 31) / 32));
   L.part = take(((n + kEmbedSeg - 1) / kEmbedSeg) * 2 * static_cast<size_t>(H) * sizeof(float));
   if (N > kSortMost) {
     const size_t nblk = (n + kCompactThreads - 1) / kCompactThreads;
@@ -92,12 +94,12 @@ cudaError_t launch_dependent(Kern k, dim3 grid, dim3 block, cudaStream_t st, Arg
 }
 
 // Blocks of embed_join along its list.
-constexpr unsigned kJoinBlocks = 64;
+constexpr int kJoinBlocks = 64;
 
-template <class TIn, class TOut, int kVec>
-cudaError_t run_sums(const void* d_out, int64_t N, int H, int64_t padding, float scale,
-                     int accumulate, void* d_weight, char* w, const EmbedLayout& L,
-                     cudaStream_t st) {
+template <class TIn, class TOut, int kVec, bool kZeroVec>
+cudaError_t run_sums(const void* d_out, int64_t N, int H, int64_t V, int64_t padding, float scale,
+                     int accumulate, void* d_weight, const ZeroPlan& z, char* w,
+                     const EmbedLayout& L, cudaStream_t st) {
   const uint32_t* keys = reinterpret_cast<const uint32_t*>(w + L.keys);
   const int* vals = reinterpret_cast<const int*>(w + L.vals);
   const long long* n_valid = reinterpret_cast<const long long*>(w + L.n_valid);
@@ -106,22 +108,45 @@ cudaError_t run_sums(const void* d_out, int64_t N, int H, int64_t padding, float
   int* joins = reinterpret_cast<int*>(w + L.joins);
   // an id that no live token has, where there is no padding_idx
   const uint32_t pad = padding >= 0 ? static_cast<uint32_t>(padding) : 0xffffffffu;
-  const unsigned segs = static_cast<unsigned>((N + kEmbedSeg - 1) / kEmbedSeg);
-  const auto cols = [H](int threads) {
-    return static_cast<unsigned>((H + threads * kVec - 1) / (threads * kVec));
-  };
-  cudaError_t e = launch_dependent(embed_segments_kernel<TIn, TOut, kVec>,
-                                   dim3(segs, cols(kEmbedThreads)), dim3(kEmbedThreads), st, keys,
-                                   vals, n_valid, static_cast<const TIn*>(d_out), H, pad, scale,
-                                   accumulate, static_cast<TOut*>(d_weight), part, join_count,
-                                   joins);
-  if (e == cudaSuccess)
-    e = launch_dependent(embed_join_kernel<TOut, kVec>,
-                         dim3(std::min(segs, kJoinBlocks), cols(kJoinCols)),
-                         dim3(kJoinCols, kJoinWays), st, keys, n_valid, H, scale, accumulate,
+  const int segs = static_cast<int>((N + kEmbedSeg - 1) / kEmbedSeg);
+  const auto cols = [H](int threads) { return (H + threads * kVec - 1) / (threads * kVec); };
+  const int ranges = z.chunks > 0 ? (z.chunks + z.range - 1) / z.range : 0;
+  const int adders = segs * cols(kEmbedThreads);
+  cudaError_t e = launch_dependent(
+      embed_segments_kernel<TIn, TOut, kVec, kZeroVec>,
+      dim3(static_cast<unsigned>(adders + ranges * (z.last - z.first))), dim3(kEmbedThreads), st,
+      segs, adders, z, V, keys, vals, n_valid, static_cast<const TIn*>(d_out), H, pad, scale,
+      accumulate, static_cast<TOut*>(d_weight), part, join_count, joins);
+  const int along = segs > 1 ? std::min(segs, kJoinBlocks) : 0;  // (one segment joins nothing)
+  const int joiners = along * cols(kJoinCols), zeros = ranges * (z.range - z.last);
+  if (e == cudaSuccess && joiners + zeros > 0)
+    e = launch_dependent(embed_join_kernel<TOut, kVec, kZeroVec>,
+                         dim3(static_cast<unsigned>(joiners + zeros)), dim3(kJoinCols * kJoinWays),
+                         st, along, joiners, z, V, keys, n_valid, H, scale, accumulate,
                          static_cast<TOut*>(d_weight), static_cast<const float*>(part),
                          static_cast<const int*>(join_count), static_cast<const int*>(joins));
   return e;
+}
+
+// Where the zeros go: about as many bytes beside the sort and the join as are
+// written while those run (the sort about 6 us and 3 ns a token, the join 15 us, at
+// about 6 TB/s), the rest beside the sums.  All of them with the first launch
+// where it does not sort.
+// 16384 tokens of a 131072 x 4096 bf16 gradient: 222 us, and 234 with all zeros in the
+// first launch.
+ZeroPlan zero_plan(int64_t N, int64_t V, int H, size_t elem, int ranges, bool sorts,
+                   uint32_t* touched) {
+  ZeroPlan z{};
+  z.touched = touched;
+  z.chunks = static_cast<int>((V + 31) / 32);
+  z.range = (z.chunks + ranges - 1) / ranges;
+  z.first = z.last = z.range;
+  if (!sorts || N == 0) return z;
+  const double chunk = 32.0 * H * static_cast<double>(elem) * ranges;  // a chunk of each range
+  const auto share = [chunk](double us) { return static_cast<int>(us * 6e6 / chunk) + 1; };
+  z.first = std::min(z.range, share(6.0 + 3e-3 * static_cast<double>(N)));
+  z.last = std::max(z.first, z.range - share(15.0));
+  return z;
 }
 
 template <class TOut>
@@ -175,17 +200,21 @@ cudaError_t run_embed_backward(DevInfo* d, const void* d_out, bool in_bf16, cons
     }
     if (e != cudaSuccess) return e;
   }
+  const bool zvec = reinterpret_cast<uintptr_t>(d_weight) % 16 == 0 &&
+                    (static_cast<size_t>(H) * sizeof(TOut)) % 16 == 0;
+  ZeroPlan z{};
   if (one_block || !accumulate) {
-    const bool vec = reinterpret_cast<uintptr_t>(d_weight) % 16 == 0 &&
-                     (static_cast<size_t>(H) * sizeof(TOut)) % 16 == 0;
-    const auto k = vec ? embed_sort_zero_kernel<TOut, true> : embed_sort_zero_kernel<TOut, false>;
+    const auto k = zvec ? embed_sort_zero_kernel<TOut, true> : embed_sort_zero_kernel<TOut, false>;
     e = set_smem_attr(k, kSortSmem);
     if (e != cudaSuccess) return e;
-    const size_t smem = one_block ? kSortSmem : kZeroRange / 8;
+    const int sort = one_block ? 1 : 0;
+    if (!accumulate)
+      z = zero_plan(a.N, a.V, H, sizeof(TOut), d->sms - sort, one_block,
+                    reinterpret_cast<uint32_t*>(w + L.touched));
+    const size_t smem = one_block ? kSortSmem : kZeroWords * sizeof(uint32_t);
     const int grid = accumulate ? 1 : d->sms;
     e = launch(kHelper, st, [&] {
-      k<<<grid, kSortThreads, smem, st>>>(a, sorted_keys, sorted_vals, one_block ? 1 : 0,
-                                          accumulate ? 0 : 1, padding, H,
+      k<<<grid, kSortThreads, smem, st>>>(a, sorted_keys, sorted_vals, sort, z, padding, H,
                                           static_cast<TOut*>(d_weight));
     });
     if (e != cudaSuccess) return e;
@@ -194,11 +223,14 @@ cudaError_t run_embed_backward(DevInfo* d, const void* d_out, bool in_bf16, cons
   const int vec = embed_vec(H, {d_out, d_weight});
   const auto sums = [&](auto in) {
     using TIn = decltype(in);
-    if (vec == 8)
-      return run_sums<TIn, TOut, 8>(d_out, a.N, H, padding, scale, accumulate, d_weight, w, L, st);
-    if (vec == 4)
-      return run_sums<TIn, TOut, 4>(d_out, a.N, H, padding, scale, accumulate, d_weight, w, L, st);
-    return run_sums<TIn, TOut, 1>(d_out, a.N, H, padding, scale, accumulate, d_weight, w, L, st);
+    // (vector loads of 8 or 4 elements imply the zeros' 16-byte stores, but for
+    // bf16 rows of a multiple of 4)
+    const auto run = zvec ? (vec == 8 ? run_sums<TIn, TOut, 8, true>
+                                      : (vec == 4 ? run_sums<TIn, TOut, 4, true>
+                                                  : run_sums<TIn, TOut, 1, true>))
+                          : (vec == 4 ? run_sums<TIn, TOut, 4, false>
+                                      : run_sums<TIn, TOut, 1, false>);
+    return run(d_out, a.N, H, a.V, padding, scale, accumulate, d_weight, z, w, L, st);
   };
   return in_bf16 ? sums(__nv_bfloat16{}) : sums(float{});
 }
@@ -238,7 +270,7 @@ flce_status flce_embedding_forward(const void* weight, const int64_t* ids, int64
 }
 
 size_t flce_embedding_workspace_bytes(int64_t N, int64_t H, int64_t V) {
-  return embed_sizes_ok(N, H, V) ? embed_layout(N, H).end : 0;
+  return embed_sizes_ok(N, H, V) ? embed_layout(N, H, V).end : 0;
 }
 
 flce_status flce_embedding_backward(const void* d_out, const int64_t* ids, int64_t N, int64_t H,
@@ -259,7 +291,7 @@ flce_status flce_embedding_backward(const void* d_out, const int64_t* ids, int64
       reinterpret_cast<uintptr_t>(ids) % 8 != 0 ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return FLCE_ERR_ARG;
-  const EmbedLayout L = embed_layout(N, H);
+  const EmbedLayout L = embed_layout(N, H, V);
   if (workspace_bytes < L.end) return FLCE_ERR_WORKSPACE;
   DevInfo* d = nullptr;
   const flce_status s = device_info(&d);

@@ -117,45 +117,52 @@ __global__ void __launch_bounds__(kLookupThreads)
 }
 
 // ---------------------------------------------------------------- zeros
-// Zeros of the rows [v0, v1) of d_weight that no live token touches (padding_idx
-// counts as untouched).  Each range's touched rows are collected in a bit map by
-// reading all ids.  kVec 16-byte stores where rows are whole multiples of them.
-constexpr int kZeroRange = 32768;
+// The rows that no live token touches (padding_idx counts as untouched) are zeroed in
+// chunks of 32 rows, spread over the launches of the call so that stores go on while
+// the sort, the sums and the join wait for their loads: chunk c of its range
+// belongs to the first launch if c < first, to embed_join if c >= last, else to
+// embed_segments.  A range is the chunks that one block of the first launch maps: it
+// reads all ids and writes a word of touched rows for each.
+struct ZeroPlan {
+  uint32_t* touched;  // [chunks]
+  int chunks;         // of the weight; 0: nothing is zeroed (accumulating calls)
+  int range;          // chunks of a range
+  int first, last;
+};
+constexpr int kZeroWords = 1024;  // of a range's map at a time
 
+// Rows [32 c, 32 c + 32) of d_weight whose bit is not set, a warp per row.  kVec: 16-byte
+// stores, where rows are whole multiples of them.
 template <class TOut, bool kVec>
-__device__ __forceinline__ void zero_untouched(const int64_t* ids, int N, int64_t ignore_index,
-                                               int64_t padding_idx, int64_t v0, int64_t v1, int H,
-                                               TOut* d_weight, uint32_t* bits) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / 32;
-  for (; v0 < v1; v0 += kZeroRange) {
-    const int rows = static_cast<int>(v1 - v0 < kZeroRange ? v1 - v0 : kZeroRange);
-    __syncthreads();
-    for (int i = threadIdx.x; i < (rows + 31) / 32; i += blockDim.x) bits[i] = 0u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < N; i += blockDim.x) {
-      const int64_t id = ids[i];
-      if (id >= v0 && id < v0 + rows && id != ignore_index && id != padding_idx)
-        atomicOr(&bits[(id - v0) >> 5], 1u << ((id - v0) & 31));
-    }
-    __syncthreads();
-    for (int r = warp; r < rows; r += warps) {
-      if ((bits[r >> 5] >> (r & 31)) & 1u) continue;
-      TOut* o = d_weight + static_cast<size_t>(v0 + r) * H;
-      if constexpr (kVec) {
-        const int n = H * static_cast<int>(sizeof(TOut)) / 16;
-        for (int c = lane; c < n; c += 32) reinterpret_cast<uint4*>(o)[c] = make_uint4(0, 0, 0, 0);
-      } else {
-        for (int c = lane; c < H; c += 32) o[c] = TOut(0.f);
-      }
+__device__ __forceinline__ void zero_chunk(uint32_t touched, int c, int64_t V, int H,
+                                           TOut* d_weight, int warps) {
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < 32; r += warps) {
+    const int64_t v = static_cast<int64_t>(c) * 32 + r;
+    if (v >= V) return;
+    if ((touched >> r) & 1u) continue;
+    TOut* o = d_weight + static_cast<size_t>(v) * H;
+    if constexpr (kVec) {
+      const int n = H * static_cast<int>(sizeof(TOut)) / 16;
+      for (int k = lane; k < n; k += 32) reinterpret_cast<uint4*>(o)[k] = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int k = lane; k < H; k += 32) o[k] = TOut(0.f);
     }
   }
 }
 
-// Block 0 sorts (if `sort`), the others (or all) zero their share of the rows: at
-// 16384 tokens of a 131072 x 4096 bf16 gradient the sort is hidden behind those writes.
+// Chunk number i of those that belong to [from, to) of every range.
+template <class TOut, bool kVec>
+__device__ __forceinline__ void zero_share(const ZeroPlan& z, int from, int to, int i, int64_t V,
+                                           int H, TOut* d_weight, int threads) {
+  const int c = i / (to - from) * z.range + from + i % (to - from);
+  if (c < z.chunks) zero_chunk<TOut, kVec>(z.touched[c], c, V, H, d_weight, threads / 32);
+}
+
+// Block 0 sorts (if `sort`); the others, or all, map one range each and zero its first share.
 template <class TOut, bool kVec>
 __global__ void __launch_bounds__(kSortThreads)
-    embed_sort_zero_kernel(const SortArgs a, uint32_t* keys, int* vals, int sort, int zero,
+    embed_sort_zero_kernel(const SortArgs a, uint32_t* keys, int* vals, int sort, const ZeroPlan z,
                            int64_t padding_idx, int H, TOut* __restrict__ d_weight) {
   extern __shared__ __align__(16) uint8_t smem_dyn[];
   griddep_launch_dependents();
@@ -166,10 +173,27 @@ __global__ void __launch_bounds__(kSortThreads)
     });
     return;
   }
-  if (!zero) return;
-  const int64_t b = static_cast<int>(blockIdx.x) - sort, n = static_cast<int>(gridDim.x) - sort;
-  zero_untouched<TOut, kVec>(a.ids, a.N, a.ignore_index, padding_idx, a.V * b / n,
-                             a.V * (b + 1) / n, H, d_weight, reinterpret_cast<uint32_t*>(smem_dyn));
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem_dyn);
+  const int64_t begin = static_cast<int64_t>(static_cast<int>(blockIdx.x) - sort) * z.range;
+  const int64_t end = min(begin + z.range, static_cast<int64_t>(z.chunks));
+  for (int64_t c0 = begin; c0 < end; c0 += kZeroWords) {
+    const int words = static_cast<int>(min(end - c0, static_cast<int64_t>(kZeroWords)));
+    const int64_t v0 = c0 * 32;
+    __syncthreads();
+    for (int i = threadIdx.x; i < words; i += kSortThreads) bits[i] = 0u;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.N; i += kSortThreads) {
+      const int64_t id = a.ids[i];
+      if (id >= v0 && id < v0 + static_cast<int64_t>(words) * 32 && id < a.V &&
+          id != a.ignore_index && id != padding_idx)
+        atomicOr(&bits[(id - v0) >> 5], 1u << ((id - v0) & 31));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < words; i += kSortThreads) z.touched[c0 + i] = bits[i];
+    for (int i = 0; i < words && c0 + i - begin < z.first; ++i)
+      zero_chunk<TOut, kVec>(bits[i], static_cast<int>(c0 + i), a.V, H, d_weight,
+                             kSortThreads / 32);
+  }
 }
 
 // ---------------------------------------------------------------- sums
@@ -214,9 +238,11 @@ __device__ __forceinline__ void embed_put(TOut* d_weight, uint32_t v, int H, int
   store_vec<kVec>(o, x);
 }
 
-template <class TIn, class TOut, int kVec>
+// Blocks 0 .. segs * (column blocks) - 1 add, those behind them zero.
+template <class TIn, class TOut, int kVec, bool kZeroVec>
 __global__ void __launch_bounds__(kEmbedThreads)
-    embed_segments_kernel(const uint32_t* keys, const int* vals,
+    embed_segments_kernel(int segs, int adders, const ZeroPlan z, int64_t V,
+                          const uint32_t* keys, const int* vals,
                           const long long* n_valid, const TIn* __restrict__ d_out,
                           int H, uint32_t padding, float scale, int accumulate, TOut* d_weight,
                           float* part, int* join_count, int* joins) {
@@ -224,8 +250,14 @@ __global__ void __launch_bounds__(kEmbedThreads)
   __shared__ int val[kEmbedSeg];
   griddep_wait();
   griddep_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= adders) {
+    zero_share<TOut, kZeroVec>(z, z.first, z.last, static_cast<int>(blockIdx.x) - adders, V, H,
+                               d_weight, kEmbedThreads);
+    return;
+  }
+  const int seg_id = static_cast<int>(blockIdx.x) % segs, col_id = static_cast<int>(blockIdx.x) / segs;
   const long long nv = *n_valid;
-  const long long s0 = static_cast<long long>(blockIdx.x) * kEmbedSeg;
+  const long long s0 = static_cast<long long>(seg_id) * kEmbedSeg;
   if (s0 >= nv) return;
   const int n = static_cast<int>(nv - s0 < kEmbedSeg ? nv - s0 : kEmbedSeg);
   constexpr uint32_t kNone = 0xffffffffu;
@@ -235,15 +267,15 @@ __global__ void __launch_bounds__(kEmbedThreads)
     if (i < kEmbedSeg) val[i] = vals[s0 + min(i, n - 1)];  // (past the end: the last one again)
   }
   __syncthreads();
-  if (blockIdx.y == 0 && threadIdx.x == 0) {
+  if (col_id == 0 && threadIdx.x == 0) {
     const uint32_t last = key[n];
     const bool whole = key[0] == last && key[1] == last;  // began in an earlier segment
     if (n == kEmbedSeg && key[n + 1] == last && !whole && last != padding)
-      joins[atomicAdd(join_count, 1)] = static_cast<int>(blockIdx.x);
+      joins[atomicAdd(join_count, 1)] = seg_id;
   }
-  const int col = (blockIdx.y * kEmbedThreads + threadIdx.x) * kVec;
+  const int col = (col_id * kEmbedThreads + static_cast<int>(threadIdx.x)) * kVec;
   if (col >= H) return;
-  float* seg = part + static_cast<size_t>(blockIdx.x) * 2 * H + col;
+  float* seg = part + static_cast<size_t>(seg_id) * 2 * H + col;
   const TIn* src = d_out + col;
   float sum[kVec];
 #pragma unroll
@@ -281,18 +313,25 @@ __global__ void __launch_bounds__(kEmbedThreads)
 constexpr int kJoinWays = 8;
 constexpr int kJoinCols = 32;  // threads along the columns
 
-template <class TOut, int kVec>
+// Blocks 0 .. adders - 1 (`along` of them along the list) add, those behind them zero.
+template <class TOut, int kVec, bool kZeroVec>
 __global__ void __launch_bounds__(kJoinWays * kJoinCols)
-    embed_join_kernel(const uint32_t* keys, const long long* n_valid, int H, float scale,
+    embed_join_kernel(int along, int adders, const ZeroPlan z, int64_t V,
+                      const uint32_t* keys, const long long* n_valid, int H, float scale,
                       int accumulate, TOut* d_weight, const float* part, const int* join_count,
                       const int* joins) {
   __shared__ float sums[kJoinWays][kJoinCols][kVec + 1];
   griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= adders) {
+    zero_share<TOut, kZeroVec>(z, z.last, z.range, static_cast<int>(blockIdx.x) - adders, V, H,
+                               d_weight, kJoinWays * kJoinCols);
+    return;
+  }
   const int count = *join_count;
   const long long nv = *n_valid;
-  const int x = threadIdx.x, y = threadIdx.y, t = y * kJoinCols + x;
-  const int col = (blockIdx.y * kJoinCols + x) * kVec;
-  for (int j = blockIdx.x; j < count; j += gridDim.x) {
+  const int t = threadIdx.x, x = t % kJoinCols, y = t / kJoinCols;
+  const int col = (static_cast<int>(blockIdx.x) / along * kJoinCols + x) * kVec;
+  for (int j = static_cast<int>(blockIdx.x) % along; j < count; j += along) {
     const int seg = joins[j];
     const long long end = static_cast<long long>(seg + 1) * kEmbedSeg;
     const uint32_t id = keys[end - 1];
