@@ -34,9 +34,16 @@ struct ScorePlan {
   bool compact;    // rows without a token are left out of the GEMM
 };
 
-// Tiles of 256 columns with softcap, whose long epilogue a 512-column tile exposes
-// (777 x 3584 x 256000: 1.06 against 1.11 ms), else as the forward's.
-ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k, bool softcap) {
+// Tiles of 256 columns, whose epilogue runs beside the next tile's MMAs, where a
+// 512-column tile would expose a long one: with softcap (777 x 3584 x 256000: 1.06 against 1.11
+// ms), and with alternatives over short K loops (top 8, 8192 x 2048 x 32000: 0.83 against
+// 0.93 ms; top 4, 1024 x 2048 x 131072: 0.46 against 0.54).  Else as the forward's, 512
+// (top 4, 300 x 4096 x 131072: 0.36 against 0.38 ms; none, 8192 x 2048 x 32000: 0.72
+// against 0.76).
+constexpr int64_t kShortH = 2048;
+
+ScorePlan score_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, int top_k,
+                     bool softcap) {
   ScorePlan P{};
   P.K = static_cast<int>(std::min<int64_t>(top_k + kTopMargin, V));
   P.cap = bf16 ? top_list_cap(P.K) : P.K;
@@ -45,7 +52,7 @@ ScorePlan score_plan(const Opts& o, int64_t N, int64_t V, bool bf16, int top_k, 
     return P;
   }
   P.cta_group = (o.cta_group == 1 || N <= kFewRows) ? 1 : 2;
-  P.bn = P.cta_group == 1 || softcap ? 256 : o.fwd_bn;
+  P.bn = P.cta_group == 1 || softcap || (top_k > 0 && H <= kShortH) ? 256 : o.fwd_bn;
   P.compact = N > kFewRows && o.fwd_compact;
   const int64_t unit_rows = BM * P.cta_group, workers = kPlanSms / P.cta_group;
   const int64_t mt = std::max<int64_t>((N + unit_rows - 1) / unit_rows, 1);
@@ -267,8 +274,8 @@ size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dt
   if (top_k < 0 || top_k > FLCE_MAX_TOP_K || top_k > V) return 0;
   const bool bf16 = dtype == FLCE_BF16;
   const Opts o = opts();
-  return std::max(score_layout(score_plan(o, N, V, bf16, top_k, false), N, H).end,
-                  score_layout(score_plan(o, N, V, bf16, top_k, true), N, H).end);
+  return std::max(score_layout(score_plan(o, N, H, V, bf16, top_k, false), N, H).end,
+                  score_layout(score_plan(o, N, H, V, bf16, top_k, true), N, H).end);
 }
 
 flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,
@@ -289,7 +296,7 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   if (N > 0 && (tokens == nullptr) != (logprobs == nullptr)) return FLCE_ERR_ARG;
   if (N > 0 && top_k > 0 && (top_logprobs == nullptr || top_ids == nullptr)) return FLCE_ERR_ARG;
   const bool bf16 = dtype == FLCE_BF16;
-  const ScorePlan P = score_plan(o, N, V, bf16, top_k, softcap > 0.f);
+  const ScorePlan P = score_plan(o, N, H, V, bf16, top_k, softcap > 0.f);
   const ScoreLayout L = score_layout(P, N, H);
   if (workspace_bytes < L.end) return FLCE_ERR_WORKSPACE;
   DevInfo* d = nullptr;
