@@ -533,3 +533,41 @@ def test_backward_of_few_tokens_cuts_the_vocabulary(N, H, V):
             assert G.rel_l2(x.cpu().numpy(), r) <= t
         # two fp32 roundings of sums of at most about 8
         assert (acc - (base + first[0])).abs().max() <= 1e-5
+
+
+@pytest.mark.parametrize("N,H,V", [(17000, 16, 300), (5000, 8, 3000), (16385, 8, 40)])
+def test_many_rows(N, H, V):
+    """More rows than one block orders, more row tiles than a raster group."""
+    host, dev = problem(N, H, V, seed=N, n_ign=N // 3)
+    got = flce.logprobs_forward(*dev, top_k=3, check_status=True)
+    check_forward(got, host, top_k=3)
+    a = np.random.default_rng(31).standard_normal(N).astype(np.float32)
+    grads = flce.logprobs_backward(*dev, got.saved, torch.from_numpy(a).cuda(), check_status=True)
+    tol = gradient_tolerance(host[0], host[1], ref.dz(*host, a, None, IGN), host[2])
+    for g, r, t in zip(grads, ref.backward(*host, a, None, IGN), tol):
+        assert G.rel_l2(g.cpu().numpy(), r) <= t
+
+
+@pytest.mark.parametrize("order", ["random", "rising"])
+def test_long_runs_of_a_large_vocabulary(order):
+    """Lists of 36 for 4096 rows take the longer runs; a sample of rows is checked."""
+    N, H, V = 4096, 8, 131072
+    g = np.random.default_rng(32)
+    h = fi.bf16_to_f32(fi.bf16_round(g.standard_normal((N, H)).astype(np.float32)))
+    w = fi.bf16_to_f32(fi.bf16_round(g.standard_normal((V, H)).astype(np.float32)))
+    if order == "rising":  # every block of columns brings better ones (bf16 has 8 bits each)
+        h = np.abs(h)
+        w[:] = 0.0
+        w[:, 0] = np.arange(V) // 512
+        w[:, 1] = (np.arange(V) % 512) // 2 / 256
+        h[:, 0] = 1.0
+    y = g.integers(0, V, N)
+    host, dev = on_gpu(h, w, y)
+    got = flce.logprobs_forward(*dev, top_k=32, check_status=True)
+    rows = np.concatenate([[0, 127, 128, 255, 256, N - 1], g.integers(0, N, 26)])
+    f = ref.forward(h[rows], w, y[rows], IGN, 0.0, 1.0, 32)
+    t_lse, t_ent = tolerances(h[rows], w, 0.0, 1.0, f)
+    assert np.array_equal(got.top_ids.cpu().numpy()[rows], f["top_ids"])
+    assert np.abs(got.logprobs.cpu().numpy()[rows] - f["logprobs"]).max() <= t_lse
+    assert np.abs(got.top_logprobs.cpu().numpy()[rows] - f["top_logprobs"]).max() <= t_lse
+    assert np.abs(got.entropy.cpu().numpy()[rows] - f["entropy"]).max() <= t_ent

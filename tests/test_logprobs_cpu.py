@@ -73,6 +73,11 @@ def test_workspace_bytes(lib):
         assert ws(n, 64, 512, 0, top_k) % 256 == 0
     assert ws(5000, 64, 512, 0, 8) > ws(5000, 64, 512, 0, 0)
     assert ws(0, 64, 512, 0, 4) > 0
+    # longer runs of tiles bound the lists: at most 16 tiles of 256 columns (softcap), so 512 / 16
+    # runs and about 10 short ones, two lists of 96 entries each for 16384 rows: 1.06e9 bytes,
+    # and the rows' hidden states, 1.3e8
+    assert ws(16384, 4096, 131072, 0, 32) < 5 << 28
+    assert ws(4096, 4096, 131072, 0, 8) < 700 << 20
 
 
 def _fwd(lib, N=64, H=64, V=512, softcap=0.0, temperature=1.0, top_k=4, dtype=0, hidden=FAKE,
