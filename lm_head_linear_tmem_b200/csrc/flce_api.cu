@@ -354,7 +354,7 @@ int64_t dh_split_rows(const Opts& o, int64_t N, int64_t V) {
       align_up(std::min<int64_t>(chunking(o, N, V).tc, std::max<int64_t>(N, 1)), 256));
 }
 
-// Backward counters of one call, zeroed at its start: a dynamic tile counter
+// Backward counters of one call, zeroed at its start with the header before them: a dynamic tile counter
 // for each GEMM launch (at most three per chunk), then one per chunk that the
 // CTAs of its gradient launches count themselves out on.
 int64_t bwd_counters(const Opts& o, int64_t N, int64_t V) { return 4 * bwd_chunks(o, N, V); }
@@ -834,10 +834,6 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
   const int nchunks = static_cast<int>(bwd_chunks(o, N, V));
   int* done = counters + 3 * nchunks;  // per chunk: CTAs of its gradient launches that finished
   std::vector<int> readers(nchunks, 0);  // per chunk: CTAs of its gradient launches
-  {
-    const cudaError_t e = cudaMemsetAsync(counters, 0, 4 * bwd_counters(o, N, V), st);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
 
   // Row compaction: the GEMMs see the valid token rows first (compact hidden,
   // labels and lse), the device-side count bounds their token-row dimension,
@@ -1211,7 +1207,11 @@ flce_status backward_any(const void* hidden, const void* weight, const int64_t* 
   s = device_info(&d);
   if (s != FLCE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(unsigned int), st);  // status word
+  // status word, and the tensor-core path's counters behind the header
+  const size_t clear = (dtype == FLCE_BF16 && N > 0)
+                           ? kHeaderBytes + 4 * static_cast<size_t>(bwd_counters(o, N, V))
+                           : sizeof(unsigned int);
+  cudaError_t e = cudaMemsetAsync(workspace, 0, clear, st);
   if (e != cudaSuccess) return cuda_fail(e);
   if (N == 0) {
     if (d_weight == nullptr || (flags & FLCE_ACCUMULATE_DWEIGHT)) return FLCE_OK;  // adds nothing
@@ -1256,22 +1256,20 @@ flce_status backward_any(const void* hidden, const void* weight, const int64_t* 
     s = backward_fp32(d, hidden, weight, labels, lse, N, H, V, ignore_index, softcap, reduction,
                       grad_output, gscale, nv, dh32, dw32, inner, st, rg);
   if (s != FLCE_OK) return s;
-  const struct {
-    int32_t flag, acc;
-    const float* src;
-    void* dst;
-    size_t n;
-  } outs[2] = {{FLCE_DHIDDEN_BF16, FLCE_ACCUMULATE_DHIDDEN, dh32, d_hidden,
-                static_cast<size_t>(N) * H},
-               {FLCE_DWEIGHT_BF16, FLCE_ACCUMULATE_DWEIGHT, dw32, d_weight,
-                static_cast<size_t>(V) * H}};
-  for (const auto& out : outs) {
-    if (!(flags & out.flag) || out.dst == nullptr) continue;
+  RoundArgs r[2] = {};
+  int n_round = 0;
+  if (d_hidden != nullptr && (flags & FLCE_DHIDDEN_BF16))
+    r[n_round++] = RoundArgs{dh32, reinterpret_cast<__nv_bfloat16*>(d_hidden),
+                             static_cast<size_t>(N) * H, (flags & FLCE_ACCUMULATE_DHIDDEN) ? 1 : 0};
+  if (d_weight != nullptr && (flags & FLCE_DWEIGHT_BF16))
+    r[n_round++] = RoundArgs{dw32, reinterpret_cast<__nv_bfloat16*>(d_weight),
+                             static_cast<size_t>(V) * H, (flags & FLCE_ACCUMULATE_DWEIGHT) ? 1 : 0};
+  if (n_round > 0) {
+    const size_t most = std::max(r[0].n, r[1].n);
     const unsigned blocks = static_cast<unsigned>(
-        std::min<size_t>((out.n / 8 + 255) / 256 + 1, static_cast<size_t>(d->sms) * 8));
+        std::min<size_t>((most / 8 + 255) / 256 + 1, static_cast<size_t>(d->sms) * 8));
     e = launch(kHelper, st, [&] {
-      f32_to_bf16_kernel<<<blocks, 256, 0, st>>>(out.src, static_cast<__nv_bfloat16*>(out.dst),
-                                                 out.n, (flags & out.acc) ? 1 : 0);
+      f32_to_bf16_kernel<<<dim3(blocks, n_round), 256, 0, st>>>(r[0], r[1]);
     });
     if (e != cudaSuccess) return cuda_fail(e);
   }

@@ -195,10 +195,21 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ bf16 outputs
 // dst[i] = bf16(src[i]) or, accumulating, bf16(float(dst[i]) + src[i]); one
 // round-to-nearest-even per element.  8 elements per thread step when both
-// pointers are 16-byte aligned, else one.
+// pointers are 16-byte aligned, else one.  Grid row 0 rounds r0, row 1 (if any) r1.
+struct RoundArgs {
+  const float* src;
+  __nv_bfloat16* dst;
+  size_t n;
+  int accumulate;
+};
+
 __global__ void __launch_bounds__(256)
-    f32_to_bf16_kernel(const float* __restrict__ src, __nv_bfloat16* __restrict__ dst, size_t n,
-                       int accumulate) {
+    f32_to_bf16_kernel(const RoundArgs r0, const RoundArgs r1) {
+  const RoundArgs& a = blockIdx.y == 0 ? r0 : r1;
+  const float* __restrict__ src = a.src;
+  __nv_bfloat16* __restrict__ dst = a.dst;
+  const size_t n = a.n;
+  const int accumulate = a.accumulate;
   const size_t stride = static_cast<size_t>(gridDim.x) * blockDim.x;
   const size_t t = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const bool vec = ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15u) == 0;

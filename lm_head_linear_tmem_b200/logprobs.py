@@ -41,7 +41,7 @@ def logprobs_forward(hidden: torch.Tensor, weight: torch.Tensor,
                      tokens: Optional[torch.Tensor] = None, ignore_index: int = -100,
                      softcap: float = 0.0, temperature: float = 1.0, top_k: int = 0,
                      workspace: Optional[torch.Tensor] = None,
-                     check_status: bool = False) -> Logprobs:
+                     check_status: bool = False, *, _own_storage: bool = False) -> Logprobs:
     """Scores hidden [..., H] with the LM head weight [V, H] (bfloat16 or float32).
 
     tokens [...]: the given tokens; rows whose token is ignore_index take no part
@@ -63,15 +63,16 @@ def logprobs_forward(hidden: torch.Tensor, weight: torch.Tensor,
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     else:
         check_workspace(workspace, dev)
-    # outputs of their own (not views of one buffer: a caller may change them in place)
-    def rows(*more, dtype=torch.float32):
-        return torch.empty(lead + more, dtype=dtype, device=dev)
-
-    saved = torch.empty((2, N), dtype=torch.float32, device=dev)
-    logprobs = None if y is None else rows()
-    entropy, lse = rows(), rows()
-    top_lp = rows(k) if k else None
-    top_ids = rows(k, dtype=torch.int64) if k else None
+    if _own_storage:  # an autograd function's outputs, which a caller may change in place
+        saved = torch.empty((2, N), dtype=torch.float32, device=dev)
+        entropy, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(2))
+        logprobs = None if y is None else torch.empty_like(lse)
+    else:  # one allocation
+        f = torch.empty((4 if y is None else 5, *lead), dtype=torch.float32, device=dev)
+        entropy, lse, *rest = f[2:].unbind(0)
+        saved, logprobs = f[:2].view(2, N), rest[0] if rest else None
+    top_lp = torch.empty((*lead, k), dtype=torch.float32, device=dev) if k else None
+    top_ids = torch.empty((*lead, k), dtype=torch.int64, device=dev) if k else None
     with on_device(dev):
         st = _lib().flce_logprobs_forward(
             _ptr(h2), _ptr(w), _ptr(y), N, H, V, int(ignore_index), float(softcap),
@@ -139,7 +140,8 @@ def logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.
 class _LogprobsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, hidden, weight, tokens, ignore_index, softcap, temperature, top_k):
-        out = logprobs_forward(hidden, weight, tokens, ignore_index, softcap, temperature, top_k)
+        out = logprobs_forward(hidden, weight, tokens, ignore_index, softcap, temperature, top_k,
+                               _own_storage=True)
         ctx.save_for_backward(hidden, weight, tokens, out.saved)
         ctx.cfg = (ignore_index, softcap, temperature)
         ctx.mark_non_differentiable(*(t for t in out[2:] if t is not None))
