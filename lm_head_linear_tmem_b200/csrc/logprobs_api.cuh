@@ -45,7 +45,7 @@ constexpr int64_t kShortH = 2048;
 ScorePlan score_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, int top_k,
                      bool softcap) {
   ScorePlan P{};
-  P.K = static_cast<int>(std::min<int64_t>(top_k + kTopMargin, V));
+  P.K = static_cast<int>(std::min<int64_t>(top_k > 0 ? top_k + kTopMargin : kPlainList, V));
   P.cap = bf16 ? top_list_cap(P.K) : P.K;
   if (!bf16) {
     P.slots = static_cast<int>((V + kScoreCols - 1) / kScoreCols);

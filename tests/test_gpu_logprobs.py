@@ -571,3 +571,30 @@ def test_long_runs_of_a_large_vocabulary(order):
     assert np.abs(got.logprobs.cpu().numpy()[rows] - f["logprobs"]).max() <= t_lse
     assert np.abs(got.top_logprobs.cpu().numpy()[rows] - f["top_logprobs"]).max() <= t_lse
     assert np.abs(got.entropy.cpu().numpy()[rows] - f["entropy"]).max() <= t_ent
+
+
+@pytest.mark.parametrize("top_k,several", [(0, 1), (1, 4), (8, 4), (20, 16)])
+def test_dominant_tokens_at_fp64_accuracy(top_k, several):
+    """Rows whose probability sits in a few tokens with logits of 12 to 20, where H = 4096
+    truncated partial sums cost 1e-4: as many as are kept (2 without alternatives,
+    else top_k + 4) are taken from fp64, so that lse and log probabilities are fp32
+    numbers of size up to 20 (half a step 1e-6) from sums in fp32 (2^-22 of log 2 and
+    2^-22 relative, twice): 3e-6, and 2e-6 more for the rest of the probability (a tenth at
+    most, off by its truncation of at most 2e-5)."""
+    N, H, V = 64, 4096, 4000
+    g = torch.Generator(device="cuda").manual_seed(33 + top_k)
+    w = (0.02 * torch.randn(V, H, device="cuda", generator=g)).to(torch.bfloat16)
+    t = torch.stack([torch.randperm(V, device="cuda", generator=g)[:several] for _ in range(N)])
+    h = torch.randn(N, H, device="cuda", generator=g)
+    for j in range(several):
+        h += 16.0 / (4e-4 * H) * w[t[:, j]].float()
+    h = h.to(torch.bfloat16)
+    f = flce.logprobs_forward(h, w, t[:, 0].contiguous(), top_k=top_k)
+    z = h.double() @ w.double().t()
+    lse = torch.logsumexp(z, -1)
+    lp = z.gather(1, t[:, :1])[:, 0] - lse
+    p = torch.log_softmax(z, -1)
+    ent = -(p.exp() * p).sum(-1)
+    assert float((f.lse - lse).abs().max()) <= 5e-6
+    assert float((f.logprobs - lp).abs().max()) <= 5e-6
+    assert float((f.entropy - ent).abs().max()) <= 5e-6 * (1 + float(ent.max()))
