@@ -132,8 +132,8 @@ flce_status check_score(const Opts& o, const void* hidden, const void* weight, i
 }
 
 // Threads that score_finish gives each row: 512 up to kFinishFewRows rows (two for
-// every SM), where a row's latency is what counts (32 rows, K = 24: 55 us with 128);
-// else 64, or 128 from kFinishManyDots dot products (8192 rows, K = 4: 70 against 93 us;
+// every SM), where a row's latency is what counts (32 rows, K = 24: 55 us with 128), and
+// 1024 where 16 warps would take its dot products in two rounds; else 64, or 128 from kFinishManyDots dot products (8192 rows, K = 4: 70 against 93 us;
 // 4096 rows, K = 12: 187 against 140).
 constexpr int kFinishFewRows = 2 * kPlanSms;
 constexpr int kFinishManyDots = 8;
@@ -161,7 +161,9 @@ cudaError_t run_finish_with(const void* hidden, const void* weight, const Finish
 template <class T>
 cudaError_t run_finish(const void* hidden, const void* weight, const FinishArgs& a,
                        cudaStream_t st) {
-  if (a.N <= kFinishFewRows) return run_finish_with<T, 512>(hidden, weight, a, st);
+  if (a.N <= kFinishFewRows)
+    return a.K + 1 > 512 / 32 ? run_finish_with<T, 1024>(hidden, weight, a, st)
+                              : run_finish_with<T, 512>(hidden, weight, a, st);
   return a.K + 1 >= kFinishManyDots ? run_finish_with<T, 128>(hidden, weight, a, st)
                                     : run_finish_with<T, 64>(hidden, weight, a, st);
 }

@@ -8,7 +8,7 @@ namespace flce {
 
 // Tokens in (id, token) order, those without an id (ignored, or out of range) behind
 // the others: a stable radix sort, digits of `digit_bits` bits, by one block in shared
-// memory.  Up to kSortMost tokens it does in one launch, of about 10 us at 4096 tokens, what the
+// memory.  Up to kSortMost tokens it does in one launch, of 16 us at 4096 tokens, what the
 // kernels of small_kernels.cuh do in one per step of every digit; more tokens
 // go through those.
 constexpr int kSortThreads = 1024;
@@ -177,7 +177,8 @@ __device__ __forceinline__ void sort_block(const SortArgs& a, uint8_t* smem, con
     __syncthreads();
   }
   const int fin = a.passes & 1;
-  for (int i = t; i < a.N; i += kSortThreads) put(i, key[fin][i], static_cast<int>(val[fin][i]), live_sum);
+  for (int i = t; i < a.N; i += kSortThreads)
+    put(i, key[fin][i], static_cast<int>(val[fin][i]), live_sum);
   if (t == 0) *a.n_valid = live_sum;
 }
 
