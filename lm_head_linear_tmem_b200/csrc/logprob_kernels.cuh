@@ -415,16 +415,15 @@ struct ScoreEpi {
 };
 
 // ------------------------------------------------------------------ fp32 inputs
-// Partial results of kRows rows x kScoreCols columns per block (slot = column
+// Partial results of kRows rows x kCols columns per block (slot = column
 // block): each warp computes the logits of four columns at a time against all
 // rows (hidden rows in shared memory, the weight read once per block), then one
 // warp per row reduces them.
-constexpr int kScoreCols = 256;
 constexpr int kScoreThreads = 256;
 
 // kVec: 4 where H is a multiple of 4 (hidden and weight rows are then 16-byte
 // aligned), else 1.
-template <int kRows, int kVec>
+template <int kRows, int kCols, int kVec>
 __global__ void __launch_bounds__(kScoreThreads)
     score_simt_kernel(const float* __restrict__ hidden, const float* __restrict__ weight, int N,
                       int H, int V, float softcap, float scale, int slots, int K, int cap,
@@ -432,10 +431,11 @@ __global__ void __launch_bounds__(kScoreThreads)
                       TopEntry* __restrict__ lists) {
   extern __shared__ __align__(16) float sh[];
   float* hs = sh;               // [kRows][H]
-  float* zs = sh + kRows * H;   // [kRows][kScoreCols]
-  const int row0 = blockIdx.y * kRows, v0 = blockIdx.x * kScoreCols;
-  const int rows = min(kRows, N - row0), cols = min(kScoreCols, V - v0);
+  float* zs = sh + kRows * H;   // [kRows][kCols]
+  const int row0 = blockIdx.y * kRows, v0 = blockIdx.x * kCols;
+  const int rows = min(kRows, N - row0), cols = min(kCols, V - v0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 8
   for (int i = threadIdx.x; i < kRows * H; i += kScoreThreads)
     hs[i] = i < rows * H ? hidden[static_cast<size_t>(row0) * H + i] : 0.f;
   __syncthreads();
@@ -480,12 +480,12 @@ __global__ void __launch_bounds__(kScoreThreads)
         float a = acc[r][c];
 #pragma unroll
         for (int o = 16; o >= 1; o /= 2) a += __shfl_xor_sync(0xffffffffu, a, o);
-        if (lane == 0 && c0 + c < cols) zs[r * kScoreCols + c0 + c] = a;
+        if (lane == 0 && c0 + c < cols) zs[r * kCols + c0 + c] = a;
       }
   }
   __syncthreads();
   for (int r = warp; r < rows; r += kScoreThreads / 32) {
-    float* z = zs + r * kScoreCols;
+    float* z = zs + r * kCols;
     const size_t at = static_cast<size_t>(row0 + r) * slots + blockIdx.x;
     Stats st{kNoMax, 0.f, 0.f};
     for (int c = lane; c < cols; c += 32) st.m = fmaxf(st.m, capped(z[c], softcap) * scale);

@@ -25,7 +25,7 @@ constexpr size_t kMaxListBytes = size_t{512} << 20;
 
 struct ScorePlan {
   int cta_group;   // 1: 128 x 256 tiles of single CTAs, 2: 256-row tiles of pairs
-  int bn;          // columns of a tile
+  int bn;          // columns of a tile (fp32: of a block)
   RunMap map;      // runs of column tiles
   int runs;
   int slots;       // partial results per row
@@ -33,6 +33,11 @@ struct ScorePlan {
   int cap;         // entries of a list
   bool compact;    // rows without a token are left out of the GEMM
 };
+
+// score_simt's blocks: eight rows (two where eight rows of hidden do not fit shared
+// memory) x 256 columns, or 64 where those would not give every SM one (8 x 1000 x 8009: 23
+// against 45 us; 60 x 1000 x 8009: 81 against 62).
+constexpr int kScoreRows = 8, kScoreCols = 256, kScoreFewCols = 64;
 
 // Tiles of 256 columns, whose epilogue runs beside the next tile's MMAs, where a
 // 512-column tile would expose a long one: with softcap (777 x 3584 x 256000: 1.06 against 1.11
@@ -48,7 +53,11 @@ ScorePlan score_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, 
   P.K = static_cast<int>(std::min<int64_t>(top_k > 0 ? top_k + kTopMargin : kPlainList, V));
   P.cap = bf16 ? top_list_cap(P.K) : P.K;
   if (!bf16) {
-    P.slots = static_cast<int>((V + kScoreCols - 1) / kScoreCols);
+    P.bn = static_cast<int>(((N + kScoreRows - 1) / kScoreRows) * ((V + kScoreCols - 1) / kScoreCols) <
+                                    kPlanSms
+                                ? kScoreFewCols
+                                : kScoreCols);
+    P.slots = static_cast<int>((V + P.bn - 1) / P.bn);
     return P;
   }
   P.cta_group = (o.cta_group == 1 || N <= kFewRows) ? 1 : 2;
@@ -240,18 +249,17 @@ flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
 }
 
-// Rows per block of score_simt: eight, or two where eight rows of hidden do not
-// fit shared memory (kSimtMaxH rows of two do).
 constexpr size_t kScoreSimtSmem = 200 * 1024;
 size_t score_simt_smem(int rows, int64_t H) {
   return sizeof(float) * static_cast<size_t>(rows) * (static_cast<size_t>(H) + kScoreCols);
 }
 
-template <int kRows>
+template <int kRows, int kCols>
 cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishArgs& a,
                            float4* part, int* count, TopEntry* lists, cudaStream_t st) {
   static_assert(2 * (kSimtMaxH + kScoreCols) * sizeof(float) <= kScoreSimtSmem, "two rows fit");
-  const auto k = a.H % 4 == 0 ? score_simt_kernel<kRows, 4> : score_simt_kernel<kRows, 1>;
+  const auto k =
+      a.H % 4 == 0 ? score_simt_kernel<kRows, kCols, 4> : score_simt_kernel<kRows, kCols, 1>;
   const cudaError_t e = set_smem_attr(k, kScoreSimtSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.slots), static_cast<unsigned>((a.N + kRows - 1) / kRows));
@@ -340,9 +348,12 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   float4* part = reinterpret_cast<float4*>(w + L.part);
   int* count = reinterpret_cast<int*>(w + L.count);
   TopEntry* lists = reinterpret_cast<TopEntry*>(w + L.lists);
-  e = score_simt_smem(8, H) <= kScoreSimtSmem
-          ? run_score_simt<8>(hidden, weight, fin, part, count, lists, st)
-          : run_score_simt<2>(hidden, weight, fin, part, count, lists, st);
+  const bool eight = score_simt_smem(kScoreRows, H) <= kScoreSimtSmem;
+  const auto run = P.bn == kScoreCols
+                       ? (eight ? run_score_simt<kScoreRows, kScoreCols> : run_score_simt<2, kScoreCols>)
+                       : (eight ? run_score_simt<kScoreRows, kScoreFewCols>
+                                : run_score_simt<2, kScoreFewCols>);
+  e = run(hidden, weight, fin, part, count, lists, st);
   if (e == cudaSuccess) e = run_finish<float>(hidden, weight, fin, st);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
 }
