@@ -645,7 +645,10 @@ __global__ void __launch_bounds__(kFinishThreads)
   griddep_wait();
   const int j = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int row = a.perm != nullptr ? a.perm[j] : j;
-  bool live = a.perm == nullptr || j < *a.n_valid;
+  // After a GEMM that gave up on a wait (only the status word tells) the partial results may
+  // be unwritten memory, whose counts and ids must not be followed.
+  const bool failed = (*a.status & kStatusTimeout) != 0u;
+  bool live = !failed && (a.perm == nullptr || j < *a.n_valid);
   int64_t y = -1;
   if (a.tokens != nullptr) {
     y = a.tokens[row];

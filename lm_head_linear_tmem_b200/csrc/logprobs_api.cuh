@@ -35,8 +35,8 @@ struct ScorePlan {
 };
 
 // score_simt's blocks: eight rows (two where eight rows of hidden do not fit shared
-// memory) x 256 columns, or 64 where those would not give every SM one (8 x 1000 x 8009: 23
-// against 45 us; 60 x 1000 x 8009: 81 against 62).
+// memory) x 256 columns, or 64 where 256 would not give every SM a block (8 x 1000 x 8009:
+// 23 us with 64, 45 with 256; 60 x 1000 x 8009, the other side: 81 with 64, 62 with 256).
 constexpr int kScoreRows = 8, kScoreCols = 256, kScoreFewCols = 64;
 
 // Tiles of 256 columns, whose epilogue runs beside the next tile's MMAs, where a
@@ -140,10 +140,11 @@ flce_status check_score(const Opts& o, const void* hidden, const void* weight, i
   return FLCE_OK;
 }
 
-// Threads that score_finish gives each row: 512 up to kFinishFewRows rows (two for
-// every SM), where a row's latency is what counts (32 rows, K = 24: 55 us with 128), and
-// 1024 where 16 warps would take its dot products in two rounds; else 64, or 128 from kFinishManyDots dot products (8192 rows, K = 4: 70 against 93 us;
-// 4096 rows, K = 12: 187 against 140).
+// Threads that score_finish gives each row.  Up to kFinishFewRows rows (two for every SM),
+// where a row's latency is what counts, 512 (32 rows, K = 24: 55 us with 128), and 1024 where
+// 16 warps would take its dot products in two rounds (the same: 33 us with 512, 29 with 1024).
+// Of more rows 64, or 128 from kFinishManyDots dot products (8192 rows, K = 4: 70 us with 64, 93
+// with 128; 4096 rows, K = 12: 187 against 140).
 constexpr int kFinishFewRows = 2 * kPlanSms;
 constexpr int kFinishManyDots = 8;
 
