@@ -4,7 +4,8 @@
 //
 //   ScoreEpi        epilogue of the tcgen05 GEMM (tc_gemm.cuh): streaming softmax
 //                   statistics and the candidates for the largest logits of a row
-//   score_simt      the same partial results for float32 inputs (CUDA cores)
+//   score_simt      the same partial results for float32 inputs (CUDA cores), few rows
+//   score_tile      ... and more rows
 //   score_finish    joins a row's partial results and evaluates the outputs
 #pragma once
 
@@ -421,6 +422,25 @@ struct ScoreEpi {
 // warp per row reduces them.
 constexpr int kScoreThreads = 256;
 
+// Sums of n values over the 2 * o lanes that differ in the bits below 2 * o, halving the
+// values that a lane holds at each step (31 shuffles for 32 values, where a sum of its
+// own for each takes 160): lane l of 32 ends with value l / (32 / n) in v[0].
+template <int o, int n, int size>
+__device__ __forceinline__ void lane_sums(float (&v)[size], int lane) {
+  if constexpr (n > 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n / 2; ++i) {
+      const float keep = up ? v[i + n / 2] : v[i], send = up ? v[i] : v[i + n / 2];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+    if constexpr (o > 1) lane_sums<o / 2, n / 2>(v, lane);
+  } else {
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    if constexpr (o > 1) lane_sums<o / 2, 1>(v, lane);
+  }
+}
+
 // kVec: 4 where H is a multiple of 4 (hidden and weight rows are then 16-byte
 // aligned), else 1.
 template <int kRows, int kCols, int kVec>
@@ -440,6 +460,8 @@ __global__ void __launch_bounds__(kScoreThreads)
     hs[i] = i < rows * H ? hidden[static_cast<size_t>(row0) * H + i] : 0.f;
   __syncthreads();
   constexpr int kC = 4;
+  constexpr int kSums = kRows * kC;
+  static_assert(kSums <= 32, "a lane for every sum");
   for (int c0 = warp * kC; c0 < cols; c0 += kScoreThreads / 32 * kC) {
     float acc[kRows][kC];
 #pragma unroll
@@ -473,15 +495,12 @@ __global__ void __launch_bounds__(kScoreThreads)
           for (int i = 0; i < kVec; ++i) acc[r][c] = fmaf(h[i], wv[c][i], acc[r][c]);
       }
     }
+    float v[kSums];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        float a = acc[r][c];
-#pragma unroll
-        for (int o = 16; o >= 1; o /= 2) a += __shfl_xor_sync(0xffffffffu, a, o);
-        if (lane == 0 && c0 + c < cols) zs[r * kCols + c0 + c] = a;
-      }
+    for (int i = 0; i < kSums; ++i) v[i] = acc[i / kC][i % kC];
+    lane_sums<16, kSums>(v, lane);
+    const int at = lane / (32 / kSums), r = at / kC, c = at % kC;
+    if (lane % (32 / kSums) == 0 && c0 + c < cols) zs[r * kCols + c0 + c] = v[0];
   }
   __syncthreads();
   for (int r = warp; r < rows; r += kScoreThreads / 32) {
@@ -532,6 +551,208 @@ __global__ void __launch_bounds__(kScoreThreads)
     }
     if (lane == 0) {
       part[at] = make_float4(st.m, st.s, st.t, top);
+      count[at] = n;
+    }
+  }
+}
+
+// The same for more rows than a few: kTileRows rows x kTiles * 64 columns a block, as a
+// register-tiled product.  Stages of 64 k arrive by cp.async, three ahead; in each, four
+// groups of 128 threads take a quarter of the k with 8 x 4 products a thread, so that one
+// block keeps 16 warps busy on a 64 x 64 tile.  The groups add their sums one after another
+// into zs, from which a warp reduces a row at a time.
+// 60 x 4096 x 32000: 0.58 ms (1.50 by score_simt, which reads the weight once per 8 rows);
+// 4096 x 1000 x 32000: 8.2 ms, half the rate of the multiply-adds.  The other half goes to
+// operands from shared memory and the copies' instructions; groups of 64 threads with 8 x 8
+// products, packed multiply-adds, stages of 128 k and 1024 threads were no faster.
+constexpr int kTileRows = 64, kTileCols = 64, kTileK = 64, kTileStages = 4;
+constexpr int kTileThreads = 512, kTileGroups = 4, kTileTc = 4;  // columns of a thread
+constexpr int kTilePitch = kTileK + 4;  // floats; rows then start 4 banks apart
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const float* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+template <int kTiles>
+constexpr int kTileZPitch = kTiles * kTileCols + 8;
+template <int kTiles>
+constexpr size_t kTileSmem = sizeof(float) * (kTileStages * (kTileRows + kTileCols) * kTilePitch +
+                                              kTileRows * kTileZPitch<kTiles>);
+
+template <int kTiles, int kVec>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    score_tile_kernel(const float* __restrict__ hidden, const float* __restrict__ weight, int N,
+                      int H, int V, float softcap, float scale, int slots, int K, int cap,
+                      float4* __restrict__ part, int* __restrict__ count,
+                      TopEntry* __restrict__ lists) {
+  extern __shared__ __align__(16) float sh[];
+  constexpr int kStage = (kTileRows + kTileCols) * kTilePitch;
+  constexpr int kZ = kTileZPitch<kTiles>, kCols = kTiles * kTileCols;
+  float* zs = sh + kTileStages * kStage;  // [kTileRows][kZ]
+  const int row0 = blockIdx.y * kTileRows, v0 = blockIdx.x * kCols;
+  const int rows = min(kTileRows, N - row0), cols = min(kCols, V - v0);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int tiles = (cols + kTileCols - 1) / kTileCols;
+
+  // The next stage to load: k block at lk of column tile lt, zeros past the rows, the columns
+  // and H.  A thread's four vectors are at one k of rows 32 apart, so that what is left
+  // to do for each is an addition, two selections and the copy (the addresses worked out anew
+  // took as many instructions as the products).
+  constexpr int kQ = kTileK / 4, kEach = kTileThreads / kQ;
+  static_assert(kTileRows == 2 * kEach && kTileCols == 2 * kEach, "vectors of a thread");
+  const int lr = t / kQ, lq = 4 * (t % kQ);
+  const float* src[4];
+  int lim[4];  // k below which there is something to load
+  const auto point = [&](int e, const float* base, int row, int end) {
+    src[e] = base + (row < end ? static_cast<size_t>(row) * H : 0) + lq;
+    lim[e] = row < end ? H - lq : 0;
+  };
+  const auto point_cols = [&](int c0) {
+    point(2, weight, c0 + lr, V);
+    point(3, weight, c0 + lr + kEach, V);
+  };
+  point(0, hidden, row0 + lr, N);
+  point(1, hidden, row0 + lr + kEach, N);
+  point_cols(v0);
+  int lk = 0, lt = 0, ls = 0;
+  const uint32_t dst0 = smem_u32(sh + lr * kTilePitch + lq);
+  const auto load = [&] {
+    if (lt < tiles) {
+      const uint32_t dst = dst0 + static_cast<uint32_t>(ls * kStage * 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* from = lk < lim[e] ? src[e] + lk : hidden;
+        const uint32_t to = dst + static_cast<uint32_t>(e * kEach * kTilePitch * 4);
+        if constexpr (kVec == 4) {
+          cp_async_16(to, from, lk < lim[e] ? 16 : 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            cp_async_4(to + 4u * j, lk + j < lim[e] ? from + j : hidden, lk + j < lim[e] ? 4 : 0);
+        }
+      }
+      ls = ls + 1 < kTileStages ? ls + 1 : 0;
+      lk += kTileK;
+      if (lk >= H) {
+        lk = 0;
+        ++lt;
+        point_cols(v0 + lt * kTileCols);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kTileStages - 1; ++i) load();
+
+  constexpr int kTx = kTileCols / kTileTc, kGroup = 8 * kTx;
+  static_assert(kGroup * kTileGroups == kTileThreads, "threads");
+  const int group = t / kGroup, ty = t % kGroup / kTx, tx = t % kTx;
+  float acc[8][kTileTc];
+  const float* a0 = sh + ty * kTilePitch + group * (kTileK / kTileGroups);
+  const float* b0 = sh + (kTileRows + tx) * kTilePitch + group * (kTileK / kTileGroups);
+  int stage = 0;
+  for (int tile = 0; tile < tiles; ++tile) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < kTileTc; ++c) acc[r][c] = 0.f;
+    for (int k = 0; k < H; k += kTileK) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kTileStages - 2) : "memory");
+      __syncthreads();  // this stage is there, and the one before it has been read
+      load();
+      const float *a = a0 + stage * kStage, *b = b0 + stage * kStage;
+      stage = stage + 1 < kTileStages ? stage + 1 : 0;
+#pragma unroll
+      for (int q = 0; q < kTileK / 4 / kTileGroups; ++q) {
+        float4 av[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          av[r] = *reinterpret_cast<const float4*>(a + r * 8 * kTilePitch + 4 * q);
+#pragma unroll
+        for (int c = 0; c < kTileTc; ++c) {
+          const float4 bv =
+              *reinterpret_cast<const float4*>(b + c * kTx * kTilePitch + 4 * q);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            acc[r][c] = fmaf(av[r].x, bv.x, acc[r][c]);
+            acc[r][c] = fmaf(av[r].y, bv.y, acc[r][c]);
+            acc[r][c] = fmaf(av[r].z, bv.z, acc[r][c]);
+            acc[r][c] = fmaf(av[r].w, bv.w, acc[r][c]);
+          }
+        }
+      }
+    }
+    float* z = zs + ty * kZ + tile * kTileCols + tx;
+    for (int g = 0; g < kTileGroups; ++g) {
+      if (group == g)
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int c = 0; c < kTileTc; ++c) {
+            float& o = z[r * 8 * kZ + c * kTx];
+            o = g == 0 ? acc[r][c] : o + acc[r][c];
+          }
+      __syncthreads();
+    }
+  }
+
+  constexpr int kMine = kCols / 32;  // columns of a lane
+  for (int r = warp; r < rows; r += kTileThreads / 32) {
+    const size_t at = static_cast<size_t>(row0 + r) * slots + blockIdx.x;
+    float z[kMine];
+    Stats st{kNoMax, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+      z[c] = lane + 32 * c < cols ? zs[r * kZ + lane + 32 * c] : -CUDART_INF_F;
+      if (lane + 32 * c < cols) st.m = fmaxf(st.m, capped(z[c], softcap) * scale);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) st.m = fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, o));
+    uint32_t key[kMine];
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+      key[c] = z[c] > kNoMax ? order_key(z[c]) : 0u;
+      if (lane + 32 * c < cols) {
+        const float d = max_nan(fmaf(capped(z[c], softcap), scale, -st.m), kLowExp2);
+        const float e = exp2f(d);
+        st.s += e;
+        st.t = fmaf(e, d, st.t);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) {
+      st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+      st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
+    }
+    // the K largest, one after another: the lowest column of the largest key
+    int n = 0;
+    uint32_t top = 0u;
+    for (; n < K; ++n) {
+      uint32_t mine = key[0];
+#pragma unroll
+      for (int c = 1; c < kMine; ++c) mine = max(mine, key[c]);
+      const uint32_t best = __reduce_max_sync(0xffffffffu, mine);
+      if (best == 0u) break;
+      if (n == 0) top = best;
+      bool taken = false;
+#pragma unroll
+      for (int c = 0; c < kMine; ++c) {
+        const uint32_t have = __ballot_sync(0xffffffffu, !taken && key[c] == best);
+        if (have != 0u && !taken) {
+          taken = true;
+          if (lane == __ffs(have) - 1) {
+            key[c] = 0u;
+            lists[at * cap + n] = TopEntry{order_value(best), v0 + 32 * c + lane};
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      part[at] = make_float4(st.m, st.s, st.t, order_value(top));
       count[at] = n;
     }
   }

@@ -31,13 +31,21 @@ struct ScorePlan {
   int slots;       // partial results per row
   int K;           // large logits kept for each row
   int cap;         // entries of a list
+  int tiles;       // fp32: column tiles of a score_tile block; 0: score_simt
   bool compact;    // rows without a token are left out of the GEMM
 };
 
 // score_simt's blocks: eight rows (two where eight rows of hidden do not fit shared
-// memory) x 256 columns, or 64 where 256 would not give every SM a block (8 x 1000 x 8009:
-// 23 us with 64, 45 with 256; 60 x 1000 x 8009, the other side: 81 with 64, 62 with 256).
-constexpr int kScoreRows = 8, kScoreCols = 256, kScoreFewCols = 64;
+// memory) x 64 columns (8 x 1000 x 8009: 29 us, and 55 with 256, for which most SMs get no
+// block; 8 x 4096 x 131072: 0.873 and 0.879 ms).
+constexpr int kScoreRows = 8, kScoreCols = 64;
+// More rows than this are score_tile's: 16 x 4096 x 32000 takes 0.45 ms by score_simt, and
+// 0.55 by tiles of 64 rows (24 rows: 0.86 against 0.55; 24 x 1000 x 8009: 49 against 51 us).
+constexpr int kTileFrom = 16;
+// Column tiles of a block: 1, or kWideTiles where that still leaves kWideFrom blocks for every
+// SM, which means longer lists but fewer of them (4096 x 1000 x 32000, K = 12: 9.7 ms
+// with 1, 9.0 with 4; 500 x 1000 x 10007: 0.39 with 1, 0.48 with 4).
+constexpr int kWideTiles = 4, kWideFrom = 8;
 
 // Tiles of 256 columns, whose epilogue runs beside the next tile's MMAs, where a
 // 512-column tile would expose a long one: with softcap (777 x 3584 x 256000: 1.06 against 1.11
@@ -52,11 +60,16 @@ ScorePlan score_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, 
   ScorePlan P{};
   P.K = static_cast<int>(std::min<int64_t>(top_k > 0 ? top_k + kTopMargin : kPlainList, V));
   P.cap = bf16 ? top_list_cap(P.K) : P.K;
+  if (!bf16 && N > kTileFrom) {
+    const int64_t blocks = (N + kTileRows - 1) / kTileRows * ((V + kWideTiles * kTileCols - 1) /
+                                                              (kWideTiles * kTileCols));
+    P.tiles = blocks >= kWideFrom * kPlanSms ? kWideTiles : 1;
+    P.bn = P.tiles * kTileCols;
+    P.slots = static_cast<int>((V + P.bn - 1) / P.bn);
+    return P;
+  }
   if (!bf16) {
-    P.bn = static_cast<int>(((N + kScoreRows - 1) / kScoreRows) * ((V + kScoreCols - 1) / kScoreCols) <
-                                    kPlanSms
-                                ? kScoreFewCols
-                                : kScoreCols);
+    P.bn = kScoreCols;
     P.slots = static_cast<int>((V + P.bn - 1) / P.bn);
     return P;
   }
@@ -255,17 +268,32 @@ size_t score_simt_smem(int rows, int64_t H) {
   return sizeof(float) * static_cast<size_t>(rows) * (static_cast<size_t>(H) + kScoreCols);
 }
 
-template <int kRows, int kCols>
+template <int kRows>
 cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishArgs& a,
                            float4* part, int* count, TopEntry* lists, cudaStream_t st) {
   static_assert(2 * (kSimtMaxH + kScoreCols) * sizeof(float) <= kScoreSimtSmem, "two rows fit");
   const auto k =
-      a.H % 4 == 0 ? score_simt_kernel<kRows, kCols, 4> : score_simt_kernel<kRows, kCols, 1>;
+      a.H % 4 == 0 ? score_simt_kernel<kRows, kScoreCols, 4> : score_simt_kernel<kRows, kScoreCols, 1>;
   const cudaError_t e = set_smem_attr(k, kScoreSimtSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.slots), static_cast<unsigned>((a.N + kRows - 1) / kRows));
   return launch(kSimt, st, [&] {
     k<<<grid, kScoreThreads, score_simt_smem(kRows, a.H), st>>>(
+        static_cast<const float*>(hidden), static_cast<const float*>(weight), a.N, a.H, a.V,
+        a.softcap, a.scale, a.slots, a.K, a.cap, part, count, lists);
+  });
+}
+
+template <int kTiles>
+cudaError_t run_score_tile(const void* hidden, const void* weight, const FinishArgs& a,
+                           float4* part, int* count, TopEntry* lists, cudaStream_t st) {
+  const auto k = a.H % 4 == 0 ? score_tile_kernel<kTiles, 4> : score_tile_kernel<kTiles, 1>;
+  const cudaError_t e = set_smem_attr(k, kTileSmem<kTiles>);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(a.slots),
+                  static_cast<unsigned>((a.N + kTileRows - 1) / kTileRows));
+  return launch(kSimt, st, [&] {
+    k<<<grid, kTileThreads, kTileSmem<kTiles>, st>>>(
         static_cast<const float*>(hidden), static_cast<const float*>(weight), a.N, a.H, a.V,
         a.softcap, a.scale, a.slots, a.K, a.cap, part, count, lists);
   });
@@ -350,10 +378,11 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   int* count = reinterpret_cast<int*>(w + L.count);
   TopEntry* lists = reinterpret_cast<TopEntry*>(w + L.lists);
   const bool eight = score_simt_smem(kScoreRows, H) <= kScoreSimtSmem;
-  const auto run = P.bn == kScoreCols
-                       ? (eight ? run_score_simt<kScoreRows, kScoreCols> : run_score_simt<2, kScoreCols>)
-                       : (eight ? run_score_simt<kScoreRows, kScoreFewCols>
-                                : run_score_simt<2, kScoreFewCols>);
+  const auto run =
+      P.tiles == kWideTiles ? run_score_tile<kWideTiles>
+      : P.tiles == 1        ? run_score_tile<1>
+      : eight               ? run_score_simt<kScoreRows>
+                            : run_score_simt<2>;
   e = run(hidden, weight, fin, part, count, lists, st);
   if (e == cudaSuccess) e = run_finish<float>(hidden, weight, fin, st);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);

@@ -101,6 +101,19 @@ def test_fp32_sizes(N, H, V, top_k, softcap, temperature):
     check_forward(got, host, softcap, temperature, top_k)
 
 
+@pytest.mark.parametrize("softcap,temperature", [(0.0, 1.0), (3.0, 0.8)])
+@pytest.mark.parametrize("N,H,V,top_k", [
+    (18, 64, 64, 2), (63, 65, 63, 32), (64, 128, 129, 0), (65, 8, 130, 5), (130, 1001, 300, 7),
+    (33, 12288, 70, 3), (17, 12, 1, 1), (600, 8, 32007, 6), (577, 67, 33000, 0)])
+def test_fp32_sizes_of_many_rows(N, H, V, top_k, softcap, temperature):
+    host, dev = problem(N, H, V, seed=N + V, n_ign=N // 5, w_std=0.1, dtype="fp32")
+    got = flce.logprobs_forward(*dev, softcap=softcap, temperature=temperature, top_k=top_k,
+                                check_status=True)
+    check_forward(got, host, softcap, temperature, top_k)
+    again = flce.logprobs_forward(*dev, softcap=softcap, temperature=temperature, top_k=top_k)
+    assert torch.equal(got.lse, again.lse) and torch.equal(got.entropy, again.entropy)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_without_tokens_every_row_is_scored(dtype):
     host, dev = problem(150, 64, 700, seed=1, n_ign=40, dtype=dtype)
