@@ -266,7 +266,9 @@ flce_status flce_backward_ex(const void* hidden, const void* weight, const int64
  * above, the places left hold id -1 and log probability -inf.  A row with nothing
  * above has lse -inf, and log probability and entropy NaN.  A NaN or +inf logit makes
  * lse, entropy and log probabilities of its row NaN (which ids a row with a NaN
- * logit lists is not defined). */
+ * logit lists is not defined).
+ * All of this holds at every temperature taken: differences of logits are divided by T, not
+ * the logits.  An lse or log probability past float32 (1e-30 makes |x| large) is infinite. */
 
 /* Largest top_k. */
 #define FLCE_MAX_TOP_K 32

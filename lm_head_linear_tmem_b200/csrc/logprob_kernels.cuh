@@ -29,9 +29,15 @@ constexpr int kMaxTopList = kMaxTopK + kTopMargin;
 constexpr int kPlainList = 2;
 
 // Logits at or below this count as -inf: masked columns, whether a mask wrote -inf or
-// the type's lowest value.  Also the running maximum that nothing has been merged
-// into (in log2 units): finite, so that the difference of two maxima is never inf - inf.
+// the type's lowest value.
 constexpr float kNoMax = -1e30f;
+// The running maximum that nothing has been merged into, a logit as well: above every
+// masked one, so that those are far below it, and finite, so that the difference of two
+// maxima is never inf - inf.
+constexpr float kNoneYet = 0.5f * kNoMax;
+// Where the temperature is so large (above 1.4e27) that even such a difference times `scale`
+// would not be a probability of 0, masked logits are made -inf first.
+constexpr float kTinyScale = 1e-27f;
 
 // Order-preserving map of the floats (no NaN) onto unsigned; 0 lies below all.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -48,25 +54,41 @@ __device__ __forceinline__ float nextbelow(float v) {
   return v == -CUDART_INF_F ? v : v == 0.f ? -1.4e-45f : order_value(order_key(v) - 1u);
 }
 
-// Statistics of a set of values x (in the log2 domain): m their maximum,
-// s = sum 2^(x - m), t = sum 2^(x - m) (x - m).  Then, in that domain,
-//   lse = m + log2 s      entropy = log2 s - t / s
+// Statistics of a set of logits L (after the softcap), scale = log2(e) / temperature: m their
+// maximum, s = sum 2^((L - m) scale), t = sum 2^((L - m) scale) (L - m) scale.  Then, in log2
+// units,
+//   lse = m scale + log2 s      entropy = log2 s - t / s
 // (t <= 0: the entropy is a sum of two non-negative terms, nothing cancels).
+// Differences are taken before they are scaled: the largest term is then 2^0 at any
+// temperature.  (A rounded m scale is off by half its step, which passes 2^7 once |m| scale
+// passes 2^31, and the largest term would be infinite or 0.)
 struct Stats {
   float m, s, t;
 };
 
-// Moves (s, t) to the maximum `m1` >= st.m.
-__device__ __forceinline__ void stats_rebase(Stats& st, float m1, float scale) {
-  st.t = (st.t + st.s * (st.m - m1)) * scale;
-  st.s *= scale;
+// A softcapped logit, tanh_z = tanh(z / softcap): a product of its own, which the compiler may
+// not join with the difference that follows (an unrounded L would not equal its maximum).
+__device__ __forceinline__ float cap_logit(float softcap, float tanh_z) {
+  return __fmul_rn(softcap, tanh_z);
+}
+
+// (L - m) scale, -inf as kLowExp2; NaN stays.
+__device__ __forceinline__ float exp2_arg(float L, float m, float scale) {
+  return max_nan((L - m) * scale, kLowExp2);
+}
+
+// Moves (s, t) to the maximum `m1` >= st.m; d = exp2_arg(st.m, m1), e = 2^d.
+__device__ __forceinline__ void stats_rebase(Stats& st, float m1, float d, float e) {
+  st.t = fmaf(st.s, d, st.t) * e;
+  st.s *= e;
   st.m = m1;
 }
 
-__device__ __forceinline__ void stats_merge(Stats& a, Stats b) {
+__device__ __forceinline__ void stats_merge(Stats& a, Stats b, float scale) {
   const float m1 = fmaxf(a.m, b.m);
-  stats_rebase(a, m1, exp2f(a.m - m1));
-  stats_rebase(b, m1, exp2f(b.m - m1));
+  const float da = exp2_arg(a.m, m1, scale), db = exp2_arg(b.m, m1, scale);
+  stats_rebase(a, m1, da, exp2f(da));
+  stats_rebase(b, m1, db, exp2f(db));
   a.s += b.s;
   a.t += b.t;
 }
@@ -340,7 +362,7 @@ struct ScoreEpi {
     p.map.of_run(run, run_start, run_len);
     const bool first = col0 == run_start * p.tile_cols;
     if (first) {
-      S.st = Stats{kNoMax, 0.f, 0.f};
+      S.st = Stats{kNoneYet, 0.f, 0.f};
       S.zmax = -CUDART_INF_F;
       S.above = row_ok ? kNoMax : CUDART_INF_F;  // rows past the end take nothing
       S.n = 0;
@@ -363,6 +385,12 @@ struct ScoreEpi {
       for (int j = 0; j < 128; ++j)
         if (j >= ncols) r[j / 32][j % 32] = __float_as_uint(-CUDART_INF_F);
     }
+    if (!kSoftcap && p.scale < kTinyScale) {
+#pragma unroll
+      for (int j = 0; j < 128; ++j)
+        if (__uint_as_float(r[j / 32][j % 32]) <= kNoMax)
+          r[j / 32][j % 32] = __float_as_uint(-CUDART_INF_F);
+    }
     float mx[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) mx[c] = max32(r[c]);
@@ -378,7 +406,7 @@ struct ScoreEpi {
 
     // ---- statistics
     if constexpr (kSoftcap) {
-      auto cap = [&](float z) { return p.softcap * tanh_exp2(z * p.inv_softcap); };
+      auto cap = [&](float z) { return cap_logit(p.softcap, tanh_exp2(z * p.inv_softcap)); };
 #pragma unroll
       for (int j = 0; j < 128; ++j)
         r[j / 32][j % 32] = __float_as_uint(cap(__uint_as_float(r[j / 32][j % 32])));
@@ -391,12 +419,13 @@ struct ScoreEpi {
       mx_all = ncols > 0 ? cap(mx_all) : -CUDART_INF_F;
     }
     Stats& st = S.st;
-    const float m1 = fmaxf(st.m, mx_all * p.scale);  // a NaN maximum (all NaN) leaves st.m
-    stats_rebase(st, m1, ex2_approx(st.m - m1));
+    const float m1 = fmaxf(st.m, mx_all);  // a NaN maximum (all NaN) leaves st.m
+    const float d1 = exp2_arg(st.m, m1, p.scale);
+    stats_rebase(st, m1, d1, ex2_approx(d1));
     float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 128; ++j) {
-      const float d = max_nan(fmaf(__uint_as_float(r[j / 32][j % 32]), p.scale, -m1), kLowExp2);
+      const float d = exp2_arg(__uint_as_float(r[j / 32][j % 32]), m1, p.scale);
       const float e = ex2_approx(d);
       s4[j & 3] += e;
       t4[j & 3] = fmaf(e, d, t4[j & 3]);
@@ -421,6 +450,11 @@ struct ScoreEpi {
 // rows (hidden rows in shared memory, the weight read once per block), then one
 // warp per row reduces them.
 constexpr int kScoreThreads = 256;
+
+// The logit that the softmax sees: after the softcap, or with masked ones as -inf.
+__device__ __forceinline__ float seen_logit(float z, float softcap) {
+  return softcap > 0.f ? cap_logit(softcap, tanhf(z / softcap)) : z <= kNoMax ? -CUDART_INF_F : z;
+}
 
 // Sums of n values over the 2 * o lanes that differ in the bits below 2 * o, halving the
 // values that a lane holds at each step (31 shuffles for 32 values, where a sum of its
@@ -506,12 +540,12 @@ __global__ void __launch_bounds__(kScoreThreads)
   for (int r = warp; r < rows; r += kScoreThreads / 32) {
     float* z = zs + r * kCols;
     const size_t at = static_cast<size_t>(row0 + r) * slots + blockIdx.x;
-    Stats st{kNoMax, 0.f, 0.f};
-    for (int c = lane; c < cols; c += 32) st.m = fmaxf(st.m, capped(z[c], softcap) * scale);
+    Stats st{kNoneYet, 0.f, 0.f};
+    for (int c = lane; c < cols; c += 32) st.m = fmaxf(st.m, seen_logit(z[c], softcap));
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) st.m = fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, o));
     for (int c = lane; c < cols; c += 32) {
-      const float d = max_nan(fmaf(capped(z[c], softcap), scale, -st.m), kLowExp2);
+      const float d = exp2_arg(seen_logit(z[c], softcap), st.m, scale);
       const float e = exp2f(d);
       st.s += e;
       st.t = fmaf(e, d, st.t);
@@ -704,11 +738,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   for (int r = warp; r < rows; r += kTileThreads / 32) {
     const size_t at = static_cast<size_t>(row0 + r) * slots + blockIdx.x;
     float z[kMine];
-    Stats st{kNoMax, 0.f, 0.f};
+    Stats st{kNoneYet, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < kMine; ++c) {
       z[c] = lane + 32 * c < cols ? zs[r * kZ + lane + 32 * c] : -CUDART_INF_F;
-      if (lane + 32 * c < cols) st.m = fmaxf(st.m, capped(z[c], softcap) * scale);
+      if (lane + 32 * c < cols) st.m = fmaxf(st.m, seen_logit(z[c], softcap));
     }
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) st.m = fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, o));
@@ -717,7 +751,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     for (int c = 0; c < kMine; ++c) {
       key[c] = z[c] > kNoMax ? order_key(z[c]) : 0u;
       if (lane + 32 * c < cols) {
-        const float d = max_nan(fmaf(capped(z[c], softcap), scale, -st.m), kLowExp2);
+        const float d = exp2_arg(seen_logit(z[c], softcap), st.m, scale);
         const float e = exp2f(d);
         st.s += e;
         st.t = fmaf(e, d, st.t);
@@ -788,8 +822,7 @@ struct FinishArgs {
   int64_t ignore_index;
   float softcap;
   double inv_temp;   // 1 / temperature
-  double nat;        // 1 / (temperature * scale)
-  float scale;       // log2(e) / temperature in fp32, as the partial results have it
+  float scale;       // log2(e) / temperature
   int slots, K, cap, top_k;  // cap: entries between one list's start and the next's
   const float4* part;
   const int* count;
@@ -840,11 +873,11 @@ template <class T>
 __device__ __forceinline__ float gemm_softcap(float z, float softcap);
 template <>
 __device__ __forceinline__ float gemm_softcap<__nv_bfloat16>(float z, float softcap) {
-  return softcap * tanh_exp2(z * (1.0f / softcap));
+  return cap_logit(softcap, tanh_exp2(z * (1.0f / softcap)));
 }
 template <>
 __device__ __forceinline__ float gemm_softcap<float>(float z, float softcap) {
-  return capped(z, softcap);
+  return cap_logit(softcap, tanhf(z / softcap));
 }
 
 // kFinishThreads: by the rows and the dot products of a row (see run_finish).
@@ -861,7 +894,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   __shared__ int ids[kMaxTopList + 1];
   __shared__ float za[kMaxTopList];
   __shared__ double zx[kMaxTopList + 1], xe[kMaxTopList + 1];
-  __shared__ double lse_sh;
+  __shared__ double max_sh, log_s_sh;  // lse's two parts (their sum may round log s away)
   static_assert(kFinishThreads % kGroups == 0 && kMaxTopList < kGroups, "groups of lists");
   griddep_wait();
   const int j = blockIdx.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -896,11 +929,11 @@ __global__ void __launch_bounds__(kFinishThreads)
   const float4* part = a.part + static_cast<size_t>(j) * a.slots;
   const int* count = a.count + static_cast<size_t>(j) * a.slots;
   const TopEntry* lists = a.lists + static_cast<size_t>(j) * a.slots * a.cap;
-  Stats st{kNoMax, 0.f, 0.f};
+  Stats st{kNoneYet, 0.f, 0.f};
   float tmax = -CUDART_INF_F;
   for (int i = t; i < a.slots; i += kFinishThreads) {
     const float4 v = part[i];
-    stats_merge(st, Stats{v.x, v.y, v.z});
+    stats_merge(st, Stats{v.x, v.y, v.z}, a.scale);
     tmax = fmaxf(tmax, v.w);
   }
   float wmax = st.m;
@@ -942,7 +975,8 @@ __global__ void __launch_bounds__(kFinishThreads)
   float M = wm[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) M = fmaxf(M, wm[w]);
-  stats_rebase(st, M, exp2f(st.m - M));
+  const float d_m = exp2_arg(st.m, M, a.scale);
+  stats_rebase(st, M, d_m, exp2f(d_m));
 #pragma unroll
   for (int o = 16; o >= 1; o /= 2) {
     st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
@@ -1052,13 +1086,13 @@ __global__ void __launch_bounds__(kFinishThreads)
       for (int o = 16; o >= 1; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
       return v;
     };
-    const double Me = static_cast<double>(st.m) * a.nat;  // the GEMM's maximum
-    double m1 = Me;
+    const double Me = static_cast<double>(st.m) * a.inv_temp;  // the GEMM's maximum
+    double m1 = -CUDART_INF;
     float s_rest = 0.f, t_rest = 0.f, z_sum = 0.f, dz_sum = 0.f;
     for (int c = lane; c < a.K; c += 32) {
       if (ids[c] < 0) continue;
       const float L = a.softcap > 0.f ? gemm_softcap<T>(za[c], a.softcap) : za[c];
-      const float d = fmaxf(fmaf(L, a.scale, -st.m), kLowExp2);
+      const float d = exp2_arg(L, st.m, a.scale);
       const float e = exp2f(d);
       s_rest += e;
       t_rest = fmaf(e, d, t_rest);
@@ -1071,23 +1105,24 @@ __global__ void __launch_bounds__(kFinishThreads)
     t_rest = st.t - sum(t_rest);
     if (s_rest < 0.f) s_rest = 0.f;
     if (t_rest > 0.f) t_rest = 0.f;
-    // The share that the truncation took of the listed logits it took, on the
-    // average, of the others too; their mean (by probability) is known, so their
-    // sum is moved by that.  At most what truncating every partial sum can take.
+    // ... and with their fp64 values, at the largest of those (the row's maximum is one of
+    // them; nothing is listed of a row that is all masked, or NaN)
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    if (m1 == -CUDART_INF) m1 = Me;
+    // The rest is moved to that maximum.  The share that the truncation took of the listed
+    // logits it took, on the average, of the others too; their mean (by probability) is known,
+    // so their sum is moved by that as well.  At most what truncating every partial sum can take.
+    float shift = static_cast<float>((Me - m1) * log2e);
     z_sum = sum(z_sum);
     dz_sum = sum(dz_sum);
     if (a.softcap == 0.f && s_rest > 0.f && z_sum > 0.f) {
       const float share = fminf(fmaxf(dz_sum / z_sum, 0.f), a.H * 0x1p-27f);
-      const float mean = st.m + t_rest / s_rest;  // log2 units
-      const float up = exp2f(share * mean);
-      if (up < 2.f && up > 0.5f) {
-        t_rest = fmaf(s_rest, share * mean, t_rest) * up;
-        s_rest *= up;
-      }
+      shift = fmaf(share, static_cast<float>(Me * log2e) + t_rest / s_rest, shift);
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
-    // ... and with their fp64 values, at the largest of those
+    // (At temperatures so low that the error of an fp32 logit divided by them counts, the
+    // difference of two maxima says nothing: the rest must not outweigh the listed ones.)
+    shift = fminf(fmaxf(shift, kLowExp2), 1.f);
     float s1 = 0.f, t1 = 0.f;
     for (int c = lane; c < a.K; c += 32) {
       if (ids[c] < 0) continue;
@@ -1096,21 +1131,22 @@ __global__ void __launch_bounds__(kFinishThreads)
       s1 += e;
       t1 = fmaf(e, d, t1);
     }
-    const float shift = static_cast<float>((Me - m1) * log2e), down = exp2f(shift);
+    const float down = exp2f(shift);
     s1 = sum(s1) + s_rest * down;
-    t1 = sum(t1) + (s_rest == 0.f ? t_rest : fmaf(s_rest, shift, t_rest)) * down;
+    t1 = sum(t1) + fmaf(s_rest, shift, t_rest) * down;
     if (lane == 0) {
       const float log2_s = log2f(s1), log2_a = log2f(st.s);  // of 0: -inf
-      const double lse = m1 + ln2 * log2_s;
-      lse_sh = lse;
-      a.lse[row] = static_cast<float>(lse);
+      max_sh = m1;
+      log_s_sh = ln2 * log2_s;
+      a.lse[row] = static_cast<float>(m1 + log_s_sh);
       a.entropy[row] = static_cast<float>(ln2) * (log2_s - t1 / s1);
       a.saved[row] = static_cast<float>(Me + ln2 * log2_a);
       a.saved[a.N + row] = static_cast<float>(ln2) * (log2_a - st.t / st.s);
     }
   }
   __syncthreads();
-  if (t == a.K && a.logprobs != nullptr) a.logprobs[row] = static_cast<float>(x - lse_sh);
+  if (t == a.K && a.logprobs != nullptr)
+    a.logprobs[row] = static_cast<float>((x - max_sh) - log_s_sh);
   if (t < a.K) {
     const int id = ids[t];
     auto ordered = [](double z) { return z != z ? -CUDART_INF : z; };  // NaN (inf - inf) last
@@ -1127,7 +1163,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     }
     if (rank < a.top_k) {
       a.top_logprobs[static_cast<size_t>(row) * a.top_k + rank] =
-          id < 0 ? -CUDART_INF_F : static_cast<float>(x - lse_sh);
+          id < 0 ? -CUDART_INF_F : static_cast<float>((x - max_sh) - log_s_sh);
       a.top_ids[static_cast<size_t>(row) * a.top_k + rank] = id;
     }
   }

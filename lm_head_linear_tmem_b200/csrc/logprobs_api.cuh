@@ -358,7 +358,6 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   fin.softcap = softcap;
   fin.inv_temp = 1.0 / temperature;
   fin.scale = scale;
-  fin.nat = 1.0 / (temperature * static_cast<double>(scale));
   fin.slots = P.slots;
   fin.K = P.K;
   fin.cap = P.cap;

@@ -34,8 +34,9 @@ def forward(hidden, weight, tokens=None, ignore_index=-100, softcap=0.0, tempera
     live, y = _live(tokens, N, V, ignore_index)
     with np.errstate(invalid="ignore", divide="ignore"):
         m = x.max(1, keepdims=True)
-        lse = (m + np.log(np.exp(x - m).sum(1, keepdims=True)))[:, 0]
-        logp = x - lse[:, None]
+        log_s = np.log(np.exp(x - m).sum(1, keepdims=True))
+        lse = (m + log_s)[:, 0]
+        logp = (x - m) - log_s  # (x - lse would lose log_s where x / T is large)
         p = np.exp(logp)
         ent = -np.where(p > 0, p * logp, np.where(np.isnan(p), np.nan, 0.0)).sum(1)
     # ties: the lowest id, so a stable sort of the ids by descending logit
@@ -58,8 +59,7 @@ def dz(hidden, weight, tokens, d_logprobs=None, d_entropy=None, ignore_index=-10
     a = np.zeros(N) if d_logprobs is None else np.where(live, d_logprobs, 0.0)
     b = np.zeros(N) if d_entropy is None else np.where(live, d_entropy, 0.0)
     m = x.max(1, keepdims=True)
-    lse = m + np.log(np.exp(x - m).sum(1, keepdims=True))
-    logp = x - lse
+    logp = (x - m) - np.log(np.exp(x - m).sum(1, keepdims=True))
     p = np.exp(logp)
     plogp = np.where(p > 0, p * logp, 0.0)
     ent = -plogp.sum(1, keepdims=True)
