@@ -298,6 +298,18 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
                                   float* top_logprobs, int64_t* top_ids, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* The same for flce_logprobs_backward_ex.
+ *   saved         device float[3 * N]    of the logits L as the matrix product rounds them: their
+ *                                        maximum m, log2 of s = sum_v exp((L_v - m) / T), and
+ *                                        the entropy */
+flce_status flce_logprobs_forward_ex(const void* hidden, const void* weight,
+                                     const int64_t* tokens, int64_t N, int64_t H, int64_t V,
+                                     int64_t ignore_index, float softcap, double temperature,
+                                     int32_t top_k, int32_t dtype, float* logprobs,
+                                     float* entropy, float* lse, float* saved,
+                                     float* top_logprobs, int64_t* top_ids, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Backward: with a_i = d_logprobs[i] and b_i = d_entropy[i] (either array may be
  * NULL: zeros),
  *   dZ_iv = ([v == y_i] a_i - p_iv (a_i + b_i (log p_iv + entropy_i))) / T
@@ -305,13 +317,29 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
  *   d_hidden = dZ . weight,  d_weight = dZ^T . hidden
  * with p and entropy from the forward's `saved`.  d_hidden, d_weight, flags and the
  * workspace (flce_workspace_bytes_ex) as flce_backward.  Gradients do not flow
- * through top_logprobs. */
+ * through top_logprobs.
+ * FLCE_BF16: dZ, a and b included, is rounded to bf16 for the two matrix products (the token's
+ * own entry is put right in float32, unless FLCE_OPT_BWD_COMPACT is 0), so gradients in float32
+ * carry that rounding too: 2^-8 of an entry of dZ at most, 3e-4 to 4e-4 of a whole gradient.
+ * An lse in float32 is off by up to 2^-24 |lse|, and every p of the row by that factor; the
+ * gradient of a token whose p is almost 1 is the difference, divided by T.  Where that counts
+ * (T below about 0.5, or logits above about 100) take the _ex forms. */
 flce_status flce_logprobs_backward(const void* hidden, const void* weight, const int64_t* tokens,
                                    const float* saved, int64_t N, int64_t H, int64_t V,
                                    int64_t ignore_index, float softcap, double temperature,
                                    int32_t dtype, const float* d_logprobs, const float* d_entropy,
                                    float* d_hidden, float* d_weight, int32_t flags,
                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same from flce_logprobs_forward_ex's `saved`, with log2 p = (L - m) log2(e) / T - log2 s:
+ * p holds to float32 rounding of the logits at any temperature. */
+flce_status flce_logprobs_backward_ex(const void* hidden, const void* weight,
+                                      const int64_t* tokens, const float* saved, int64_t N,
+                                      int64_t H, int64_t V, int64_t ignore_index, float softcap,
+                                      double temperature, int32_t dtype, const float* d_logprobs,
+                                      const float* d_entropy, float* d_hidden, float* d_weight,
+                                      int32_t flags, void* workspace, size_t workspace_bytes,
+                                      void* stream);
 
 /* ---- Embedding: rows of the [V, H] weight that the LM head shares with its
  * embedding, and the weight's gradient.

@@ -62,6 +62,12 @@ SIGNATURES = {
     "flce_logprobs_backward": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,
                                        c_f64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_size,
                                        c_vp]),
+    "flce_logprobs_forward_ex": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32,
+                                         c_f64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                         c_vp, c_size, c_vp]),
+    "flce_logprobs_backward_ex": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64,
+                                          c_f32, c_f64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32,
+                                          c_vp, c_size, c_vp]),
     "flce_embedding_forward": (c_i32, [c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_f32, c_i32, c_vp,
                                        c_vp, c_vp]),
     "flce_embedding_workspace_bytes": (c_size, [c_i64, c_i64, c_i64]),

@@ -1025,8 +1025,11 @@ flce_status backward_bf16(DevInfo* d, const Opts& o, const void* hidden, const v
                                 rg ? rg->d_logprobs : nullptr,
                                 rg ? rg->d_entropy : nullptr,
                                 rg ? rg->entropy : nullptr,
+                                rg ? rg->row_max : nullptr,
                                 perm,
-                                rg ? rg->inv_temp : 1.0f};
+                                rg ? rg->inv_temp : 1.0f,
+                                rg ? rg->scale : kLog2e,
+                                rg ? rg->lse_unit : kLog2e};
         return run_gemm<Epi, false, false>(d, o, dz_bn, kBwdDz, pz, ep, nullptr, ep, st);
       };
       if (rg != nullptr)

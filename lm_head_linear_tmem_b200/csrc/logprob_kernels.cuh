@@ -28,17 +28,6 @@ constexpr int kMaxTopList = kMaxTopK + kTopMargin;
 // cuBLAS: 5e-6 and 4e-6), with one or more alternatives 7e-8 and 2e-7.
 constexpr int kPlainList = 2;
 
-// Logits at or below this count as -inf: masked columns, whether a mask wrote -inf or
-// the type's lowest value.
-constexpr float kNoMax = -1e30f;
-// The running maximum that nothing has been merged into, a logit as well: above every
-// masked one, so that those are far below it, and finite, so that the difference of two
-// maxima is never inf - inf.
-constexpr float kNoneYet = 0.5f * kNoMax;
-// Where the temperature is so large (above 1.4e27) that even such a difference times `scale`
-// would not be a probability of 0, masked logits are made -inf first.
-constexpr float kTinyScale = 1e-27f;
-
 // Order-preserving map of the floats (no NaN) onto unsigned; 0 lies below all.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -65,17 +54,6 @@ __device__ __forceinline__ float nextbelow(float v) {
 struct Stats {
   float m, s, t;
 };
-
-// A softcapped logit, tanh_z = tanh(z / softcap): a product of its own, which the compiler may
-// not join with the difference that follows (an unrounded L would not equal its maximum).
-__device__ __forceinline__ float cap_logit(float softcap, float tanh_z) {
-  return __fmul_rn(softcap, tanh_z);
-}
-
-// (L - m) scale, -inf as kLowExp2; NaN stays.
-__device__ __forceinline__ float exp2_arg(float L, float m, float scale) {
-  return max_nan((L - m) * scale, kLowExp2);
-}
 
 // Moves (s, t) to the maximum `m1` >= st.m; d = exp2_arg(st.m, m1), e = 2^d.
 __device__ __forceinline__ void stats_rebase(Stats& st, float m1, float d, float e) {
@@ -451,10 +429,6 @@ struct ScoreEpi {
 // warp per row reduces them.
 constexpr int kScoreThreads = 256;
 
-// The logit that the softmax sees: after the softcap, or with masked ones as -inf.
-__device__ __forceinline__ float seen_logit(float z, float softcap) {
-  return softcap > 0.f ? cap_logit(softcap, tanhf(z / softcap)) : z <= kNoMax ? -CUDART_INF_F : z;
-}
 
 // Sums of n values over the 2 * o lanes that differ in the bits below 2 * o, halving the
 // values that a lane holds at each step (31 shuffles for 32 values, where a sum of its
@@ -807,9 +781,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // the vocabulary that hardly shows (small logits), but a row whose probability
 // sits in a few tokens has an lse that is one of their logits.  So the listed
 // logits' terms are taken out of (s, t) as the epilogue added them and put back
-// with their fp64 values.  The backward recomputes the uncorrected logits: it gets
-// the uncorrected lse and entropy (`saved`), with which its 1 - p of a
-// dominant token keeps its leading digits.
+// with their fp64 values.  The backward recomputes the uncorrected logits L: it gets
+// the uncorrected statistics (`saved`), the maximum m and log2 s apart: with
+// log2 p = (L - m) scale - log2 s, p of a dominant token is 1 - p to fp32 rounding at any
+// temperature (of one fp32 number of the size of L / T, half a step goes into every p: the 1 - p
+// of a certain token came out 1e-6 at T = 1 and 3e-4 at 0.01, and is divided by T).
 constexpr int kGroups = 64;  // of a row's lists, for the lower bound of the K-th best
 constexpr int kMaxHits = 512;
 constexpr int kMaxHitSlots = 256;
@@ -830,7 +806,10 @@ struct FinishArgs {
   float* logprobs;   // [N]; null without tokens
   float* entropy;    // [N]
   float* lse;        // [N]
-  float* saved;      // [2][N]: lse and entropy of the GEMM's logits
+  // of the logits that the backward sees, `saved_rows` rows of N.  3: their maximum, log2 of
+  // their sum s and the entropy; 2: lse and the entropy
+  float* saved;
+  int saved_rows;
   float* top_logprobs;  // [N, top_k]
   int64_t* top_ids;     // [N, top_k]
   unsigned int* status;
@@ -915,8 +894,7 @@ __global__ void __launch_bounds__(kFinishThreads)
       if (a.logprobs != nullptr) a.logprobs[row] = 0.f;
       a.entropy[row] = 0.f;
       a.lse[row] = 0.f;
-      a.saved[row] = 0.f;
-      a.saved[a.N + row] = 0.f;
+      for (int i = 0; i < a.saved_rows; ++i) a.saved[static_cast<size_t>(i) * a.N + row] = 0.f;
     }
     for (int i = t; i < a.top_k; i += kFinishThreads) {
       a.top_logprobs[static_cast<size_t>(row) * a.top_k + i] = 0.f;
@@ -1105,6 +1083,26 @@ __global__ void __launch_bounds__(kFinishThreads)
     t_rest = st.t - sum(t_rest);
     if (s_rest < 0.f) s_rest = 0.f;
     if (t_rest > 0.f) t_rest = 0.f;
+    // The backward's logits: the same GEMM's, or, fp32, fp64 sums rounded once (simt_logit),
+    // whose listed terms take the places of the fp32 sums' here too.
+    Stats back = st;
+    if constexpr (std::is_same_v<T, float>) {
+      float m = -CUDART_INF_F, s = 0.f, e_d = 0.f;
+      for (int c = lane; c < a.K; c += 32)
+        if (ids[c] >= 0) m = fmaxf(m, seen_logit(static_cast<float>(zx[c]), a.softcap));
+#pragma unroll
+      for (int o = 16; o >= 1; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (m == -CUDART_INF_F) m = st.m;
+      for (int c = lane; c < a.K; c += 32) {
+        if (ids[c] < 0) continue;
+        const float L = seen_logit(static_cast<float>(zx[c]), a.softcap);
+        const float d = exp2_arg(L, m, a.scale), e = exp2f(d);
+        s += e;
+        e_d = fmaf(e, d, e_d);
+      }
+      const float d = fminf(exp2_arg(st.m, m, a.scale), 1.f), e = exp2f(d);
+      back = Stats{m, sum(s) + s_rest * e, sum(e_d) + fmaf(s_rest, d, t_rest) * e};
+    }
     // ... and with their fp64 values, at the largest of those (the row's maximum is one of
     // them; nothing is listed of a row that is all masked, or NaN)
 #pragma unroll
@@ -1135,13 +1133,19 @@ __global__ void __launch_bounds__(kFinishThreads)
     s1 = sum(s1) + s_rest * down;
     t1 = sum(t1) + fmaf(s_rest, shift, t_rest) * down;
     if (lane == 0) {
-      const float log2_s = log2f(s1), log2_a = log2f(st.s);  // of 0: -inf
+      const float log2_s = log2f(s1), log2_b = log2f(back.s);  // of 0: -inf
       max_sh = m1;
       log_s_sh = ln2 * log2_s;
       a.lse[row] = static_cast<float>(m1 + log_s_sh);
       a.entropy[row] = static_cast<float>(ln2) * (log2_s - t1 / s1);
-      a.saved[row] = static_cast<float>(Me + ln2 * log2_a);
-      a.saved[a.N + row] = static_cast<float>(ln2) * (log2_a - st.t / st.s);
+      if (a.saved_rows == 3) {
+        a.saved[row] = back.m;
+        a.saved[static_cast<size_t>(a.N) + row] = log2_b;
+      } else {
+        a.saved[row] = static_cast<float>(static_cast<double>(back.m) * a.inv_temp + ln2 * log2_b);
+      }
+      a.saved[static_cast<size_t>(a.saved_rows - 1) * a.N + row] =
+          static_cast<float>(ln2) * (log2_b - back.t / back.s);
     }
   }
   __syncthreads();

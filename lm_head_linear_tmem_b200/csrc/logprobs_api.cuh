@@ -299,30 +299,13 @@ cudaError_t run_score_tile(const void* hidden, const void* weight, const FinishA
   });
 }
 
-}  // namespace
-}  // namespace flce
-
-using namespace flce;
-
-extern "C" {
-
-size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dtype,
-                                     int32_t top_k) {
-  if (dtype != FLCE_BF16 && dtype != FLCE_FP32) return 0;
-  if (!score_sizes_ok(N, H, V, dtype)) return 0;
-  if (top_k < 0 || top_k > FLCE_MAX_TOP_K || top_k > V) return 0;
-  const bool bf16 = dtype == FLCE_BF16;
-  const Opts o = opts();
-  return std::max(score_layout(score_plan(o, N, H, V, bf16, top_k, false), N, H).end,
-                  score_layout(score_plan(o, N, H, V, bf16, top_k, true), N, H).end);
-}
-
-flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,
-                                  int64_t N, int64_t H, int64_t V, int64_t ignore_index,
-                                  float softcap, double temperature, int32_t top_k, int32_t dtype,
-                                  float* logprobs, float* entropy, float* lse, float* saved,
-                                  float* top_logprobs, int64_t* top_ids, void* workspace,
-                                  size_t workspace_bytes, void* stream) {
+// The body of flce_logprobs_forward(_ex): saved_rows rows of N floats in `saved`.
+flce_status score_forward(const void* hidden, const void* weight, const int64_t* tokens, int64_t N,
+                          int64_t H, int64_t V, int64_t ignore_index, float softcap,
+                          double temperature, int32_t top_k, int32_t dtype, float* logprobs,
+                          float* entropy, float* lse, float* saved, int saved_rows,
+                          float* top_logprobs, int64_t* top_ids, void* workspace,
+                          size_t workspace_bytes, void* stream) {
   static_assert(FLCE_MAX_TOP_K == kMaxTopK, "header and kernels agree");
   const Opts o = opts();
   flce_status s = check_score(o, hidden, weight, N, H, V, softcap, temperature, dtype, workspace);
@@ -369,6 +352,7 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   fin.entropy = entropy;
   fin.lse = lse;
   fin.saved = saved;
+  fin.saved_rows = saved_rows;
   fin.top_logprobs = top_logprobs;
   fin.top_ids = top_ids;
   fin.status = ws_status(w);
@@ -387,19 +371,96 @@ flce_status flce_logprobs_forward(const void* hidden, const void* weight, const 
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
 }
 
+// saved: as flce_logprobs_forward (saved_rows 2) or flce_logprobs_forward_ex (3) wrote it.
+flce_status score_backward(const void* hidden, const void* weight, const int64_t* tokens,
+                           const float* saved, int saved_rows, int64_t N, int64_t H, int64_t V,
+                           int64_t ignore_index, float softcap, double temperature, int32_t dtype,
+                           const float* d_logprobs, const float* d_entropy, float* d_hidden,
+                           float* d_weight, int32_t flags, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!(temperature >= 1e-30) || !(temperature <= 1e30)) return FLCE_ERR_ARG;
+  RowGrads rg{};
+  rg.d_logprobs = d_logprobs;
+  rg.d_entropy = d_entropy;
+  rg.inv_temp = static_cast<float>(1.0 / temperature);
+  rg.scale = static_cast<float>(1.4426950408889634074 / temperature);
+  rg.lse_unit = saved_rows == 3 ? 1.0f : kLog2e;
+  // (a null saved is refused like a null lse)
+  const float* lse = saved;
+  if (saved != nullptr && N > 0) {
+    rg.entropy = saved + (saved_rows - 1) * N;
+    if (saved_rows == 3) {
+      rg.row_max = saved;
+      lse = saved + N;
+    }
+  }
+  return backward_any(hidden, weight, tokens, lse, N, H, V, ignore_index, softcap, FLCE_SUM, dtype,
+                      nullptr, 1.0f, -1, nullptr, d_hidden, d_weight, flags, workspace,
+                      workspace_bytes, stream, &rg);
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dtype,
+                                     int32_t top_k) {
+  if (dtype != FLCE_BF16 && dtype != FLCE_FP32) return 0;
+  if (!score_sizes_ok(N, H, V, dtype)) return 0;
+  if (top_k < 0 || top_k > FLCE_MAX_TOP_K || top_k > V) return 0;
+  const bool bf16 = dtype == FLCE_BF16;
+  const Opts o = opts();
+  return std::max(score_layout(score_plan(o, N, H, V, bf16, top_k, false), N, H).end,
+                  score_layout(score_plan(o, N, H, V, bf16, top_k, true), N, H).end);
+}
+
+flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,
+                                  int64_t N, int64_t H, int64_t V, int64_t ignore_index,
+                                  float softcap, double temperature, int32_t top_k,
+                                  int32_t dtype, float* logprobs, float* entropy, float* lse,
+                                  float* saved, float* top_logprobs, int64_t* top_ids,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  return score_forward(hidden, weight, tokens, N, H, V, ignore_index, softcap, temperature, top_k,
+                       dtype, logprobs, entropy, lse, saved, 2, top_logprobs, top_ids, workspace,
+                       workspace_bytes, stream);
+}
+
 flce_status flce_logprobs_backward(const void* hidden, const void* weight, const int64_t* tokens,
                                    const float* saved, int64_t N, int64_t H, int64_t V,
                                    int64_t ignore_index, float softcap, double temperature,
-                                   int32_t dtype, const float* d_logprobs, const float* d_entropy,
-                                   float* d_hidden, float* d_weight, int32_t flags,
-                                   void* workspace, size_t workspace_bytes, void* stream) {
-  if (!(temperature >= 1e-30) || !(temperature <= 1e30)) return FLCE_ERR_ARG;
-  // (saved: lse of every row, then entropy; a null one is refused like a null lse)
-  const RowGrads rg{d_logprobs, d_entropy, saved != nullptr && N > 0 ? saved + N : nullptr,
-                    static_cast<float>(1.0 / temperature)};
-  return backward_any(hidden, weight, tokens, saved, N, H, V, ignore_index, softcap, FLCE_SUM,
-                      dtype, nullptr, 1.0f, -1, nullptr, d_hidden, d_weight, flags, workspace,
-                      workspace_bytes, stream, &rg);
+                                   int32_t dtype, const float* d_logprobs,
+                                   const float* d_entropy, float* d_hidden, float* d_weight,
+                                   int32_t flags, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  return score_backward(hidden, weight, tokens, saved, 2, N, H, V, ignore_index, softcap,
+                        temperature, dtype, d_logprobs, d_entropy, d_hidden, d_weight, flags,
+                        workspace, workspace_bytes, stream);
+}
+
+flce_status flce_logprobs_forward_ex(const void* hidden, const void* weight, const int64_t* tokens,
+                                     int64_t N, int64_t H, int64_t V, int64_t ignore_index,
+                                     float softcap, double temperature, int32_t top_k,
+                                     int32_t dtype, float* logprobs, float* entropy, float* lse,
+                                     float* saved, float* top_logprobs, int64_t* top_ids,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  return score_forward(hidden, weight, tokens, N, H, V, ignore_index, softcap, temperature, top_k,
+                       dtype, logprobs, entropy, lse, saved, 3, top_logprobs, top_ids, workspace,
+                       workspace_bytes, stream);
+}
+
+flce_status flce_logprobs_backward_ex(const void* hidden, const void* weight, const int64_t* tokens,
+                                      const float* saved, int64_t N, int64_t H, int64_t V,
+                                      int64_t ignore_index, float softcap, double temperature,
+                                      int32_t dtype, const float* d_logprobs,
+                                      const float* d_entropy, float* d_hidden, float* d_weight,
+                                      int32_t flags, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  return score_backward(hidden, weight, tokens, saved, 3, N, H, V, ignore_index, softcap,
+                        temperature, dtype, d_logprobs, d_entropy, d_hidden, d_weight, flags,
+                        workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -709,28 +709,55 @@ __device__ __forceinline__ float simt_grad_scale(const float* grad_output, float
 }
 
 // Upstream gradients of the scoring operator (see DzEpi's kRowGrads): either
-// may be null (zero).
+// may be null (zero).  lse is relative to row_max (null: 0), in units of lse_unit log2s.
 struct RowGrads {
   const float* d_logprobs;  // [N]
   const float* d_entropy;   // [N]
   const float* entropy;     // [N]
+  const float* row_max;     // [N]
   float inv_temp;
+  float scale;
+  float lse_unit;
 };
+
+// The logit that the softmax sees: after the softcap, or with masked ones as -inf.
+__device__ __forceinline__ float seen_logit(float z, float softcap) {
+  return softcap > 0.f ? cap_logit(softcap, tanhf(z / softcap)) : z <= kNoMax ? -CUDART_INF_F : z;
+}
+
+// A row's logit in the backward.  The loss recomputes it as the forward has it.  The scoring
+// operator's forward adds in other orders, so the logits that count (the kept ones) are in
+// its saved statistics as fp64 sums rounded once, which come out the same in any order.
+template <bool kRowGrads>
+__device__ __forceinline__ float simt_logit(const float* a, const float* b, int H) {
+  if constexpr (kRowGrads) {
+    double z = 0.0;
+    for (int k = 0; k < H; ++k) z = fma(static_cast<double>(a[k]), static_cast<double>(b[k]), z);
+    return static_cast<float>(z);
+  } else {
+    float z = 0.f;
+    for (int k = 0; k < H; ++k) z = fmaf(a[k], b[k], z);
+    return z;
+  }
+}
 
 // dZ of one logit z of a row in the loss; `hit`: the row's label.
 // kRowGrads: the scoring operator's gradient, else the loss's.
 template <bool kRowGrads>
 __device__ __forceinline__ float simt_dz(float z, bool hit, float lse, float softcap, float g,
                                          const RowGrads& rg, int row) {
-  const float L = capped(z, softcap);
-  float d;
+  float L, d;
   if constexpr (kRowGrads) {
-    const float logp = max_nan(fmaf(L, rg.inv_temp, -lse), kLowExp2 * kLn2);
+    L = seen_logit(z, softcap);
+    const float m = rg.row_max != nullptr ? rg.row_max[row] : 0.f;
+    const float lp2 = max_nan(fmaf(L - m, rg.scale, -lse * rg.lse_unit), kLowExp2);  // log2 p
     const float a = rg.d_logprobs != nullptr ? rg.d_logprobs[row] : 0.f;
     const float b = rg.d_entropy != nullptr ? rg.d_entropy[row] : 0.f;
     const float e = rg.d_entropy != nullptr ? rg.entropy[row] : 0.f;
-    d = ((hit ? a : 0.f) - expf(logp) * fmaf(b, logp + e, a)) * rg.inv_temp;
+    const float q = fmaf(b, fmaf(lp2, kLn2, e), a);
+    d = fmaf(-exp2f(lp2), q, hit ? a : 0.f) * rg.inv_temp;
   } else {
+    L = capped(z, softcap);
     d = expf(L - lse) - (hit ? 1.f : 0.f);
   }
   if (softcap > 0.f) {
@@ -771,8 +798,7 @@ __global__ void __launch_bounds__(kSimtThreads)
       float gz = 0.f;
       if (valid) {
         const float* w = weight + static_cast<size_t>(v) * H;
-        float z = 0.f;
-        for (int k = 0; k < H; ++k) z = fmaf(h[k], w[k], z);
+        const float z = simt_logit<kRowGrads>(h, w, H);
         gz = simt_dz<kRowGrads>(z, v == y, l, softcap, g, rg, row);
       }
       G[j] = gz;
@@ -820,8 +846,7 @@ __global__ void __launch_bounds__(kSimtThreads)
       float gz = 0.f;
       if (y != ignore_index && y >= 0 && y < V) {  // out of range: as ignored
         const float* hi = hidden + static_cast<size_t>(i) * H;
-        float z = 0.f;
-        for (int k = 0; k < H; ++k) z = fmaf(hi[k], w[k], z);
+        const float z = simt_logit<kRowGrads>(hi, w, H);
         gz = simt_dz<kRowGrads>(z, v == y, lse[i], softcap, g, rg, i);
       }
       G[t] = gz;

@@ -112,6 +112,29 @@ constexpr float kLog2e = 1.4426950408889634f;
 // keeps (-inf) * 0 out of the sums of p log p.
 constexpr float kLowExp2 = -200.0f;
 
+// ---- scoring operator: its logits, forward and backward
+// Logits at or below this count as -inf: masked columns, whether a mask wrote -inf or
+// the type's lowest value.
+constexpr float kNoMax = -1e30f;
+// The running maximum that nothing has been merged into, a logit as well: above every
+// masked one, so that those are far below it, and finite, so that the difference of two
+// maxima is never inf - inf.
+constexpr float kNoneYet = 0.5f * kNoMax;
+// Where the temperature is so large (above 1.4e27) that even such a difference times `scale`
+// would not be a probability of 0, masked logits are made -inf first.
+constexpr float kTinyScale = 1e-27f;
+
+// A softcapped logit, tanh_z = tanh(z / softcap): a product of its own, which the compiler may
+// not join with the difference that follows (an unrounded L would not equal its maximum).
+__device__ __forceinline__ float cap_logit(float softcap, float tanh_z) {
+  return __fmul_rn(softcap, tanh_z);
+}
+
+// (L - m) scale, -inf as kLowExp2; NaN stays.
+__device__ __forceinline__ float exp2_arg(float L, float m, float scale) {
+  return max_nan((L - m) * scale, kLowExp2);
+}
+
 // tanh from one SFU exp2 and one fast division, by the identity
 // tanh(x) = sign(x) * (1 - e^{-2|x|}) / (1 + e^{-2|x|}).  e^{-2|x|} lies in
 // (0, 1] with relative (so also absolute) error about 2^-22, and the division
@@ -495,7 +518,8 @@ struct FwdStatsEpi {
 // entropy E (x = L / temperature, log p = x - lse):
 //   dZ = ([v == y] * a - p * (a + b * (log p + E))) / temperature * softcap'
 // They differ from row to row, so they go into the bf16 value; the label entry's
-// residual is taken as above.
+// residual is taken as above.  log2 p = (L - m) scale - lse', m the row's largest logit and
+// lse' = log2 sum 2^((L - m) scale): near p = 1 both differences are small numbers.
 template <bool kSoftcap, bool kRowGrads = false>
 struct DzEpi {
   using State = int;  // TMA stores issued by this warp
@@ -523,23 +547,28 @@ struct DzEpi {
     const float* d_logprobs;
     const float* d_entropy;
     const float* entropy;
+    const float* row_max;  // token order; null: 0
     const int* perm;
     float inv_temp;
+    float scale;     // log2(e) / temperature
+    float lse_unit;  // of lse, in log2 units
   };
 
   // The row's label and lse, read before the accumulator is ready.
-  // With kRowGrads also a / temperature, b / temperature and (a + b E) / temperature.
+  // With kRowGrads also a / temperature, b / temperature, (a + b E) / temperature and the
+  // logit that lse is relative to.
   struct Pre {
     int64_t y;
     float lse;
-    float a, b, c;
+    float a, b, c, m;
   };
   __device__ static Pre prepare(const Params& p, int m_base, int q, int lane) {
     const int row_l = m_base + q * 32 + lane;
-    if (row_l >= p.rows) return Pre{0, 0.f, 0.f, 0.f, 0.f};
-    Pre pre{p.labels[p.t0 + row_l], p.lse[p.t0 + row_l], 0.f, 0.f, 0.f};
+    if (row_l >= p.rows) return Pre{0, 0.f, 0.f, 0.f, 0.f, 0.f};
+    Pre pre{p.labels[p.t0 + row_l], p.lse[p.t0 + row_l], 0.f, 0.f, 0.f, 0.f};
     if constexpr (kRowGrads) {
       const int row = p.perm != nullptr ? p.perm[p.t0 + row_l] : p.t0 + row_l;
+      if (p.row_max != nullptr) pre.m = p.row_max[row];
       if (p.d_logprobs != nullptr) pre.a = p.d_logprobs[row] * p.inv_temp;
       pre.c = pre.a;
       if (p.d_entropy != nullptr) {
@@ -573,7 +602,7 @@ struct DzEpi {
       valid = (y != p.ignore_index) && y >= 0 && y < p.v_total;
       const int64_t c0 = static_cast<int64_t>(p.v0) + h0;
       if (valid && y >= c0 && y < c0 + BN / 2) y_local = static_cast<int>(y - c0);
-      lse2 = pre.lse * kLog2e;
+      lse2 = pre.lse * (kRowGrads ? p.lse_unit : kLog2e);
     }
     const uint32_t stg_u32 = smem_u32(stg);
     // warp-uniform: does any row's label fall in these columns?
@@ -583,16 +612,20 @@ struct DzEpi {
     auto dz32 = [&](int c0l, uint32_t(&r)[32]) {
       // d overwrites the logit it comes from
       if constexpr (kRowGrads) {
-        const float scale = p.inv_temp * kLog2e;
+        if (!kSoftcap && p.scale < kTinyScale) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (__uint_as_float(r[j]) <= kNoMax) r[j] = __float_as_uint(-CUDART_INF_F);
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           float L = __uint_as_float(r[j]), f = 1.0f;
           if constexpr (kSoftcap) {
-            L = p.softcap * tanh_exp2(L * p.inv_softcap);
+            L = cap_logit(p.softcap, tanh_exp2(L * p.inv_softcap));
             const float u = L * p.inv_softcap;
             f = fmaf(-u, u, 1.0f);
           }
-          const float lp2 = max_nan(fmaf(L, scale, -lse2), kLowExp2);  // log2 p
+          const float lp2 = max_nan(fmaf(L - pre.m, p.scale, -lse2), kLowExp2);  // log2 p
           const float pr = ex2_approx(lp2);
           const float qv = fmaf(pre.b * kLn2, lp2, pre.c);
           r[j] = __float_as_uint(

@@ -1,7 +1,7 @@
 """Scoring with the LM head: log probabilities of given tokens, entropy and top
 alternatives of softmax(softcap(hidden . weight^T) / temperature), without the
 [tokens, vocab] logits (argument marshalling only; the arithmetic runs in the
-CUDA library, see flce_logprobs_forward in include/flce.h).
+CUDA library, see flce_logprobs_forward_ex in include/flce.h).
 
   logprobs_forward(hidden, weight, tokens=None, ignore_index=-100, softcap=0.0,
                    temperature=1.0, top_k=0)
@@ -28,7 +28,7 @@ class Logprobs(NamedTuple):
     lse: torch.Tensor                     # float32 [...]
     top_logprobs: Optional[torch.Tensor]  # float32 [..., top_k]; None with top_k=0
     top_ids: Optional[torch.Tensor]       # int64 [..., top_k]
-    saved: torch.Tensor                   # float32 [2, N]: logprobs_backward's
+    saved: torch.Tensor                   # float32 [3, N]: logprobs_backward's
 
 
 def logprobs_workspace_bytes(N: int, H: int, V: int, dtype: torch.dtype = torch.bfloat16,
@@ -64,17 +64,17 @@ def logprobs_forward(hidden: torch.Tensor, weight: torch.Tensor,
     else:
         check_workspace(workspace, dev)
     if _own_storage:  # an autograd function's outputs, which a caller may change in place
-        saved = torch.empty((2, N), dtype=torch.float32, device=dev)
+        saved = torch.empty((3, N), dtype=torch.float32, device=dev)
         entropy, lse = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(2))
         logprobs = None if y is None else torch.empty_like(lse)
     else:  # one allocation
-        f = torch.empty((4 if y is None else 5, *lead), dtype=torch.float32, device=dev)
-        entropy, lse, *rest = f[2:].unbind(0)
-        saved, logprobs = f[:2].view(2, N), rest[0] if rest else None
+        f = torch.empty((5 if y is None else 6, *lead), dtype=torch.float32, device=dev)
+        entropy, lse, *rest = f[3:].unbind(0)
+        saved, logprobs = f[:3].view(3, N), rest[0] if rest else None
     top_lp = torch.empty((*lead, k), dtype=torch.float32, device=dev) if k else None
     top_ids = torch.empty((*lead, k), dtype=torch.int64, device=dev) if k else None
     with on_device(dev):
-        st = _lib().flce_logprobs_forward(
+        st = _lib().flce_logprobs_forward_ex(
             _ptr(h2), _ptr(w), _ptr(y), N, H, V, int(ignore_index), float(softcap),
             float(temperature), k, _DTYPES[h2.dtype], _ptr(logprobs), _ptr(entropy), _ptr(lse),
             _ptr(saved), _ptr(top_lp), _ptr(top_ids), _ptr(workspace), workspace.numel(),
@@ -115,8 +115,8 @@ def logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.
     dev = h2.device
     a = _row_grad(d_logprobs, "d_logprobs", N, dev)
     b = _row_grad(d_entropy, "d_entropy", N, dev)
-    if tuple(saved.shape) != (2, N) or saved.dtype != torch.float32 or saved.device != dev:
-        raise ValueError(f"saved must be logprobs_forward's float32 [2, {N}] tensor on {dev}")
+    if tuple(saved.shape) != (3, N) or saved.dtype != torch.float32 or saved.device != dev:
+        raise ValueError(f"saved must be logprobs_forward's float32 [3, {N}] tensor on {dev}")
     saved = saved.contiguous()
     d_hidden, d_weight, flags = alloc_grads(N, H, V, dev, d_hidden, d_weight, accumulate_d_hidden,
                                             accumulate_d_weight, grad_dtype, compute_d_hidden,
@@ -126,7 +126,7 @@ def logprobs_backward(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.
     else:
         check_workspace(workspace, dev)
     with on_device(dev):
-        st = _lib().flce_logprobs_backward(
+        st = _lib().flce_logprobs_backward_ex(
             _ptr(h2), _ptr(w), _ptr(y), _ptr(saved), N, H, V, int(ignore_index),
             float(softcap), float(temperature), _DTYPES[h2.dtype], _ptr(a), _ptr(b),
             _ptr(d_hidden), _ptr(d_weight), flags, _ptr(workspace), workspace.numel(),

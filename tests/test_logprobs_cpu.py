@@ -147,3 +147,15 @@ def test_binding_refuses_host_tensors():
         flce.logprobs_backward(h, w, y, torch.zeros(2, 2), torch.zeros(2))
     with pytest.raises(ValueError):
         flce.fused_linear_logprobs(h.requires_grad_(), w, y)
+
+
+def test_refusals_of_the_forms_with_three_saved_rows(lib):
+    """They refuse what the others do."""
+    class Ex:
+        flce_logprobs_workspace_bytes = lib.flce_logprobs_workspace_bytes
+        flce_workspace_bytes_ex = lib.flce_workspace_bytes_ex
+        flce_logprobs_forward = lib.flce_logprobs_forward_ex
+        flce_logprobs_backward = lib.flce_logprobs_backward_ex
+
+    test_forward_refusals(Ex)
+    test_backward_refusals(Ex)
