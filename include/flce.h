@@ -255,7 +255,10 @@ flce_status flce_backward_ex(const void* hidden, const void* weight, const int64
  * ids and of the given token are evaluated in float64 from the inputs, and the
  * alternatives are ordered by those (before softcap and temperature, which keep
  * the order); they are picked by float32 logits, of which at least top_k + 4 are
- * kept.  lse and entropy take the terms of the kept logits from float64 too.
+ * kept (2 with top_k = 0).  lse and entropy take the terms of the kept logits from float64 too,
+ * and with FLCE_BF16 and no softcap the others are moved by the share of their size that the
+ * tensor cores' truncation took of the kept ones (an estimate, at most H 2^-27): lse, and
+ * with it log probabilities, depend on top_k in their last digits.
  *
  * A row whose token is ignore_index takes no part: logprobs, entropy, lse and
  * top_logprobs 0, top_ids -1.  A token outside [0, V) is reported as

@@ -1108,15 +1108,19 @@ __global__ void __launch_bounds__(kFinishThreads)
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
     if (m1 == -CUDART_INF) m1 = Me;
-    // The rest is moved to that maximum.  The share that the truncation took of the listed
-    // logits it took, on the average, of the others too; their mean (by probability) is known,
-    // so their sum is moved by that as well.  At most what truncating every partial sum can take.
+    // The rest is moved to that maximum.  The share that the tensor cores' truncation took of the
+    // listed logits it took, on the average, of the others too; their mean (by probability) is
+    // known, so their sum is moved by that as well.  An estimate, capped at H 2^-27: H / 16
+    // additions, each of which takes half a step of 2^-23 on the average, of sums that grow to the
+    // logit.  (fp32 sums are rounded to nearest: their errors say nothing of the others'.)
     float shift = static_cast<float>((Me - m1) * log2e);
-    z_sum = sum(z_sum);
-    dz_sum = sum(dz_sum);
-    if (a.softcap == 0.f && s_rest > 0.f && z_sum > 0.f) {
-      const float share = fminf(fmaxf(dz_sum / z_sum, 0.f), a.H * 0x1p-27f);
-      shift = fmaf(share, static_cast<float>(Me * log2e) + t_rest / s_rest, shift);
+    if constexpr (!std::is_same_v<T, float>) {
+      z_sum = sum(z_sum);
+      dz_sum = sum(dz_sum);
+      if (a.softcap == 0.f && s_rest > 0.f && z_sum > 0.f) {
+        const float share = fminf(fmaxf(dz_sum / z_sum, 0.f), a.H * 0x1p-27f);
+        shift = fmaf(share, static_cast<float>(Me * log2e) + t_rest / s_rest, shift);
+      }
     }
     // (At temperatures so low that the error of an fp32 logit divided by them counts, the
     // difference of two maxima says nothing: the rest must not outweigh the listed ones.)
