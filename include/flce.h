@@ -371,7 +371,9 @@ size_t flce_embedding_workspace_bytes(int64_t N, int64_t H, int64_t V);
  *   padding_idx  an id whose row gets no gradient (F.embedding's); negative: none
  *   d_weight     device float[V * H], or bf16 with FLCE_DWEIGHT_BF16: overwritten (rows that no
  *                token touches become zero) or, with FLCE_ACCUMULATE_DWEIGHT, added to (other
- *                rows are not read or written): float(old) + gradient, rounded once.
+ *                rows are not read or written).  float: the gradient scale * sum is rounded to
+ *                float, then its sum with the old value is; subnormal numbers (below 1.2e-38)
+ *                may count as 0.  bf16: scale * sum + old is rounded to float, then to bf16.
  *                Accumulating into the d_weight of flce_backward or flce_logprobs_backward
  *                gives the gradient of tied weights.
  * The result does not depend on timing: a row's tokens are added in a fixed order. */

@@ -209,7 +209,9 @@ constexpr int kEmbedThreads = 128;
 // scale * sum into row v: stored, or added to what is there.  Into fp32 by
 // reductions that return nothing: no thread waits for the old value, and each
 // element gets one addition per call, so the result stays reproducible (waiting,
-// a segment of 32 different ids took 26 us).
+// a segment of 32 different ids took 26 us).  Such a reduction adds the rounded product
+// scale * sum and may flush subnormals; the loss's label terms are added to the same
+// buffer that way.
 template <class TOut, int kVec>
 __device__ __forceinline__ void embed_put(TOut* d_weight, uint32_t v, int H, int col,
                                           const float (&sum)[kVec], float scale, int accumulate) {
