@@ -210,7 +210,7 @@ flce_status flce_forward_ex2(const void* hidden, const void* weight, const int64
  *                (bf16[V*H] with FLCE_DWEIGHT_BF16)
  *                Either may be NULL: that gradient is then not computed (a
  *                frozen LM head needs no dWeight GEMM: a third of the work);
- *                at least one must be given.
+ *                at least one must be given (with N == 0, neither need be).
  *   flags        any OR of FLCE_ACCUMULATE_DHIDDEN, FLCE_ACCUMULATE_DWEIGHT,
  *                FLCE_DHIDDEN_BF16, FLCE_DWEIGHT_BF16, or 0.
  * A bf16 output is computed in fp32 scratch inside the workspace (size it with

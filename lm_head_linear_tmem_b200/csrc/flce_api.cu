@@ -1196,8 +1196,9 @@ flce_status backward_any(const void* hidden, const void* weight, const int64_t* 
   if (s != FLCE_OK) return s;
   const GradScratch gs = grad_scratch(o, N, H, V, dtype == FLCE_BF16, flags);
   if (workspace_bytes < gs.end) return FLCE_ERR_WORKSPACE;
-  // a NULL d_hidden or d_weight is not computed; one of them must be given
-  if ((d_hidden == nullptr && d_weight == nullptr) || (N > 0 && lse == nullptr))
+  // a NULL d_hidden or d_weight is not computed; one of them must be given (without tokens
+  // d_hidden has no elements, and may be NULL for that)
+  if (N > 0 && ((d_hidden == nullptr && d_weight == nullptr) || lse == nullptr))
     return FLCE_ERR_ARG;
   if (!aligned16(d_hidden) || !aligned16(d_weight)) return FLCE_ERR_ARG;
   if (!(grad_scale == grad_scale) || grad_scale == INFINITY || grad_scale == -INFINITY)
