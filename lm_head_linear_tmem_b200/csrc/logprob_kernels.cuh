@@ -806,10 +806,10 @@ struct FinishArgs {
   float* logprobs;   // [N]; null without tokens
   float* entropy;    // [N]
   float* lse;        // [N]
-  // of the logits that the backward sees, `saved_rows` rows of N.  3: their maximum, log2 of
+  // of the logits that the backward sees, saved_rows numbers saved_stride apart.  3: their maximum, log2 of
   // their sum s and the entropy; 2: lse and the entropy
   float* saved;
-  int saved_rows;
+  int saved_rows, saved_stride;
   float* top_logprobs;  // [N, top_k]
   int64_t* top_ids;     // [N, top_k]
   unsigned int* status;
@@ -894,7 +894,8 @@ __global__ void __launch_bounds__(kFinishThreads)
       if (a.logprobs != nullptr) a.logprobs[row] = 0.f;
       a.entropy[row] = 0.f;
       a.lse[row] = 0.f;
-      for (int i = 0; i < a.saved_rows; ++i) a.saved[static_cast<size_t>(i) * a.N + row] = 0.f;
+      for (int i = 0; i < a.saved_rows; ++i)
+        a.saved[static_cast<size_t>(i) * a.saved_stride + row] = 0.f;
     }
     for (int i = t; i < a.top_k; i += kFinishThreads) {
       a.top_logprobs[static_cast<size_t>(row) * a.top_k + i] = 0.f;
@@ -1144,11 +1145,11 @@ __global__ void __launch_bounds__(kFinishThreads)
       a.entropy[row] = static_cast<float>(ln2) * (log2_s - t1 / s1);
       if (a.saved_rows == 3) {
         a.saved[row] = back.m;
-        a.saved[static_cast<size_t>(a.N) + row] = log2_b;
+        a.saved[static_cast<size_t>(a.saved_stride) + row] = log2_b;
       } else {
         a.saved[row] = static_cast<float>(static_cast<double>(back.m) * a.inv_temp + ln2 * log2_b);
       }
-      a.saved[static_cast<size_t>(a.saved_rows - 1) * a.N + row] =
+      a.saved[static_cast<size_t>(a.saved_rows - 1) * a.saved_stride + row] =
           static_cast<float>(ln2) * (log2_b - back.t / back.s);
     }
   }

@@ -18,10 +18,14 @@ constexpr int kFewRows = BM;
 // share a column tile fall out of step and its weight rows leave L2 before the
 // last of them comes: 4096 x 4096 x 131072 took 2.47 ms with runs of 2, 2.54 with
 // 4 and 2.65 with 8 (8192 x 2048 x 32000: no difference).  Longer runs all the
-// same where the lists would take more than kMaxListBytes.
+// same where the lists would take more than kMaxListBytes.  Where they still take more than
+// kChunkListBytes (fp32 lists, which come in one length, too), the call works on its rows in
+// chunks that share the lists' memory: 65536 x 131072 with 32 alternatives would keep 4.3 GB of
+// them in bf16 and 9.7 GB in fp32.
 constexpr int kMaxRun = 2;
 constexpr int kLongestRun = 16;
 constexpr size_t kMaxListBytes = size_t{512} << 20;
+constexpr size_t kChunkListBytes = size_t{1} << 30;
 
 struct ScorePlan {
   int cta_group;   // 1: 128 x 256 tiles of single CTAs, 2: 256-row tiles of pairs
@@ -31,6 +35,7 @@ struct ScorePlan {
   int slots;       // partial results per row
   int K;           // large logits kept for each row
   int cap;         // entries of a list
+  int64_t rows;    // worked on at a time
   int tiles;       // fp32: column tiles of a score_tile block; 0: score_simt
   bool compact;    // rows without a token are left out of the GEMM
 };
@@ -55,9 +60,10 @@ constexpr int kWideTiles = 4, kWideFrom = 8;
 // against 0.76).
 constexpr int64_t kShortH = 2048;
 
-ScorePlan score_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, int top_k,
-                     bool softcap) {
+ScorePlan rows_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, int top_k,
+                    bool softcap) {
   ScorePlan P{};
+  P.rows = N;
   P.K = static_cast<int>(std::min<int64_t>(top_k > 0 ? top_k + kTopMargin : kPlainList, V));
   P.cap = bf16 ? top_list_cap(P.K) : P.K;
   if (!bf16 && N > kTileFrom) {
@@ -94,15 +100,31 @@ ScorePlan score_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, 
   return P;
 }
 
+size_t list_bytes(const ScorePlan& P) {
+  return sizeof(TopEntry) * static_cast<size_t>(P.rows) * P.slots * P.cap;
+}
+
+// The plan of a call: that of all its rows, or of a chunk of them.
+ScorePlan score_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, int top_k,
+                     bool softcap) {
+  ScorePlan P = rows_plan(o, N, H, V, bf16, top_k, softcap);
+  while (P.rows > 1 && list_bytes(P) > kChunkListBytes) {
+    int64_t rows = (P.rows + 1) / 2;
+    if (rows > 256) rows = static_cast<int64_t>(align_up(static_cast<size_t>(rows), 256));
+    P = rows_plan(o, rows, H, V, bf16, top_k, softcap);
+  }
+  return P;
+}
+
 // Workspace: header | group maxima (zeroed with the header) | statistics | lists |
 // row compaction.
 struct ScoreLayout {
   size_t seen, part, count, lists, perm, tokens_c, block_valid, n_valid_c, hidden_c, end;
 };
 
-ScoreLayout score_layout(const ScorePlan& P, int64_t N, int64_t H) {
+ScoreLayout score_layout(const ScorePlan& P, int64_t H) {
   ScoreLayout L{};
-  const size_t n = static_cast<size_t>(N);
+  const size_t n = static_cast<size_t>(P.rows);
   size_t off = kHeaderBytes;
   L.seen = off;
   off = align_up(off + 4 * n * P.K, 256);
@@ -299,6 +321,22 @@ cudaError_t run_score_tile(const void* hidden, const void* weight, const FinishA
   });
 }
 
+flce_status score_fp32(const ScorePlan& P, const ScoreLayout& L, const void* hidden,
+                       const void* weight, const FinishArgs& fin, char* w, cudaStream_t st) {
+  float4* part = reinterpret_cast<float4*>(w + L.part);
+  int* count = reinterpret_cast<int*>(w + L.count);
+  TopEntry* lists = reinterpret_cast<TopEntry*>(w + L.lists);
+  const bool eight = score_simt_smem(kScoreRows, fin.H) <= kScoreSimtSmem;
+  const auto run =
+      P.tiles == kWideTiles ? run_score_tile<kWideTiles>
+      : P.tiles == 1        ? run_score_tile<1>
+      : eight               ? run_score_simt<kScoreRows>
+                            : run_score_simt<2>;
+  cudaError_t e = run(hidden, weight, fin, part, count, lists, st);
+  if (e == cudaSuccess) e = run_finish<float>(hidden, weight, fin, st);
+  return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
+}
+
 // The body of flce_logprobs_forward(_ex): saved_rows rows of N floats in `saved`.
 flce_status score_forward(const void* hidden, const void* weight, const int64_t* tokens, int64_t N,
                           int64_t H, int64_t V, int64_t ignore_index, float softcap,
@@ -319,22 +357,15 @@ flce_status score_forward(const void* hidden, const void* weight, const int64_t*
   if (N > 0 && top_k > 0 && (top_logprobs == nullptr || top_ids == nullptr)) return FLCE_ERR_ARG;
   const bool bf16 = dtype == FLCE_BF16;
   const ScorePlan P = score_plan(o, N, H, V, bf16, top_k, softcap > 0.f);
-  const ScoreLayout L = score_layout(P, N, H);
+  const ScoreLayout L = score_layout(P, H);
   if (workspace_bytes < L.end) return FLCE_ERR_WORKSPACE;
   DevInfo* d = nullptr;
   s = device_info(&d);
   if (s != FLCE_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(workspace);
-  // status word and tile counter, and the group maxima behind them
-  cudaError_t e =
-      cudaMemsetAsync(w, 0, L.seen + (bf16 ? 4 * static_cast<size_t>(N) * P.K : 0), st);
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (N == 0) return FLCE_OK;
   const float scale = static_cast<float>(1.4426950408889634074 / temperature);
   FinishArgs fin{};
-  fin.tokens = tokens;
-  fin.N = static_cast<int>(N);
   fin.H = static_cast<int>(H);
   fin.V = static_cast<int>(V);
   fin.ignore_index = ignore_index;
@@ -348,27 +379,35 @@ flce_status score_forward(const void* hidden, const void* weight, const int64_t*
   fin.part = reinterpret_cast<const float4*>(w + L.part);
   fin.count = reinterpret_cast<const int*>(w + L.count);
   fin.lists = reinterpret_cast<const TopEntry*>(w + L.lists);
-  fin.logprobs = logprobs;
-  fin.entropy = entropy;
-  fin.lse = lse;
-  fin.saved = saved;
   fin.saved_rows = saved_rows;
-  fin.top_logprobs = top_logprobs;
-  fin.top_ids = top_ids;
+  fin.saved_stride = static_cast<int>(N);
   fin.status = ws_status(w);
-  if (bf16) return score_bf16(d, o, P, L, hidden, weight, tokens, fin, w, st);
-  float4* part = reinterpret_cast<float4*>(w + L.part);
-  int* count = reinterpret_cast<int*>(w + L.count);
-  TopEntry* lists = reinterpret_cast<TopEntry*>(w + L.lists);
-  const bool eight = score_simt_smem(kScoreRows, H) <= kScoreSimtSmem;
-  const auto run =
-      P.tiles == kWideTiles ? run_score_tile<kWideTiles>
-      : P.tiles == 1        ? run_score_tile<1>
-      : eight               ? run_score_simt<kScoreRows>
-                            : run_score_simt<2>;
-  e = run(hidden, weight, fin, part, count, lists, st);
-  if (e == cudaSuccess) e = run_finish<float>(hidden, weight, fin, st);
-  return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
+  int64_t row0 = 0;
+  do {
+    const int64_t n = std::min(P.rows, N - row0);
+    // tile counter, and the group maxima behind the header; the status word once
+    const size_t keep = row0 == 0 ? 0 : sizeof(unsigned int);
+    cudaError_t e = cudaMemsetAsync(
+        w + keep, 0, L.seen + (bf16 ? 4 * static_cast<size_t>(n) * P.K : 0) - keep, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (N == 0) return FLCE_OK;
+    fin.N = static_cast<int>(n);
+    fin.tokens = tokens != nullptr ? tokens + row0 : nullptr;
+    fin.logprobs = logprobs != nullptr ? logprobs + row0 : nullptr;
+    fin.entropy = entropy + row0;
+    fin.lse = lse + row0;
+    fin.saved = saved + row0;
+    if (top_k > 0) {
+      fin.top_logprobs = top_logprobs + row0 * top_k;
+      fin.top_ids = top_ids + row0 * top_k;
+    }
+    const char* hid = static_cast<const char*>(hidden) + row0 * H * (bf16 ? 2 : 4);
+    s = bf16 ? score_bf16(d, o, P, L, hid, weight, fin.tokens, fin, w, st)
+             : score_fp32(P, L, hid, weight, fin, w, st);
+    if (s != FLCE_OK) return s;
+    row0 += n;
+  } while (row0 < N);
+  return FLCE_OK;
 }
 
 // saved: as flce_logprobs_forward (saved_rows 2) or flce_logprobs_forward_ex (3) wrote it.
@@ -413,8 +452,8 @@ size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t dt
   if (top_k < 0 || top_k > FLCE_MAX_TOP_K || top_k > V) return 0;
   const bool bf16 = dtype == FLCE_BF16;
   const Opts o = opts();
-  return std::max(score_layout(score_plan(o, N, H, V, bf16, top_k, false), N, H).end,
-                  score_layout(score_plan(o, N, H, V, bf16, top_k, true), N, H).end);
+  return std::max(score_layout(score_plan(o, N, H, V, bf16, top_k, false), H).end,
+                  score_layout(score_plan(o, N, H, V, bf16, top_k, true), H).end);
 }
 
 flce_status flce_logprobs_forward(const void* hidden, const void* weight, const int64_t* tokens,

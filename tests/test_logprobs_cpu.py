@@ -159,3 +159,13 @@ def test_refusals_of_the_forms_with_three_saved_rows(lib):
 
     test_forward_refusals(Ex)
     test_backward_refusals(Ex)
+
+
+def test_lists_of_many_rows_share_memory(lib):
+    """Lists take 1 GiB at most; statistics, counts and (bf16) a chunk's hidden rows beside them."""
+    ws = lib.flce_logprobs_workspace_bytes
+    assert ws(131070, 4096, 131072, 1, 32) < 3 << 29
+    assert ws(65536, 1000, 131072, 1, 20) < 3 << 29
+    assert ws(131072, 4096, 262144, 0, 32) < 3 << 29
+    assert ws(1 << 20, 512, 131072, 0, 8) < 3 << 30   # (1 GiB of hidden rows in one chunk)
+    assert ws(131070, 4096, 131072, 1, 32) % 256 == 0
