@@ -44,7 +44,8 @@
  *
  * Conventions shared by every call:
  *  - All tensor arguments are DEVICE pointers on the current CUDA device,
- *    row-major and densely packed, 16-byte aligned (torch allocations are).
+ *    row-major and densely packed, 16-byte aligned (torch allocations are; hidden and
+ *    weight of float32 may lie on any element).
  *    hidden is [N, H], weight is [V, H], labels is int64 [N].
  *  - dtype FLCE_BF16: hidden/weight hold bfloat16; the tensor-core path runs.
  *    H must be a multiple of 8 (16-byte rows for the TMA engine).

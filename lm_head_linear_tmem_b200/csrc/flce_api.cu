@@ -456,6 +456,13 @@ long long* ws_nvalid(void* ws) {
 // ---------------------------------------------------------------- checks
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// bf16 rows go through TMA; the CUDA-core path reads fp32 ones element by element where they do
+// not start on 16-byte boundaries.
+bool inputs_aligned(const void* hidden, const void* weight, int32_t dtype) {
+  if (dtype == FLCE_BF16) return aligned16(hidden) && aligned16(weight);
+  return ((reinterpret_cast<uintptr_t>(hidden) | reinterpret_cast<uintptr_t>(weight)) & 3u) == 0;
+}
+
 flce_status check_common(const Opts& o, const void* hidden, const void* weight,
                          const int64_t* labels, int64_t N, int64_t H, int64_t V, float softcap,
                          int32_t reduction, int32_t dtype, void* ws, size_t ws_size) {
@@ -467,7 +474,7 @@ flce_status check_common(const Opts& o, const void* hidden, const void* weight,
   if (dtype == FLCE_FP32 && H > kSimtMaxH) return FLCE_ERR_SHAPE;
   if (N > 0 && (hidden == nullptr || labels == nullptr)) return FLCE_ERR_ARG;
   if (weight == nullptr || ws == nullptr) return FLCE_ERR_ARG;
-  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(ws)) return FLCE_ERR_ARG;
+  if (!inputs_aligned(hidden, weight, dtype) || !aligned16(ws)) return FLCE_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(labels) & 7u) != 0) return FLCE_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return FLCE_ERR_ARG;
   if (ws_size < ws_bytes(o, N, H, V, dtype == FLCE_BF16)) return FLCE_ERR_WORKSPACE;
@@ -1526,7 +1533,7 @@ extern "C" flce_status flce_forward_noalloc(const void* hidden, const void* weig
   if (dtype == FLCE_FP32 && H > kSimtMaxH) return FLCE_ERR_SHAPE;
   if (N > 0 && (hidden == nullptr || labels == nullptr || lse == nullptr)) return FLCE_ERR_ARG;
   if (weight == nullptr || loss == nullptr || num_tokens == nullptr) return FLCE_ERR_ARG;
-  if (!aligned16(hidden) || !aligned16(weight)) return FLCE_ERR_ARG;
+  if (!inputs_aligned(hidden, weight, dtype)) return FLCE_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(labels) & 7u) != 0) return FLCE_ERR_ARG;
   // the forward's scratch must fit the static buffer
   if (fwd_layout(N, V, dtype == FLCE_BF16).end > FLCE_NOALLOC_SCRATCH_BYTES) return FLCE_ERR_SHAPE;

@@ -449,8 +449,8 @@ __device__ __forceinline__ void lane_sums(float (&v)[size], int lane) {
   }
 }
 
-// kVec: 4 where H is a multiple of 4 (hidden and weight rows are then 16-byte
-// aligned), else 1.
+// kVec: 4 where H is a multiple of 4 and hidden and weight are 16-byte aligned (so are their
+// rows then), else 1.
 template <int kRows, int kCols, int kVec>
 __global__ void __launch_bounds__(kScoreThreads)
     score_simt_kernel(const float* __restrict__ hidden, const float* __restrict__ weight, int N,

@@ -170,7 +170,7 @@ flce_status check_score(const Opts& o, const void* hidden, const void* weight, i
   if (!score_sizes_ok(N, H, V, dtype)) return FLCE_ERR_SHAPE;
   if (N > 0 && hidden == nullptr) return FLCE_ERR_ARG;
   if (weight == nullptr || ws == nullptr) return FLCE_ERR_ARG;
-  if (!aligned16(hidden) || !aligned16(weight)) return FLCE_ERR_ARG;
+  if (!inputs_aligned(hidden, weight, dtype)) return FLCE_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return FLCE_ERR_ARG;
   return FLCE_OK;
 }
@@ -290,12 +290,18 @@ size_t score_simt_smem(int rows, int64_t H) {
   return sizeof(float) * static_cast<size_t>(rows) * (static_cast<size_t>(H) + kScoreCols);
 }
 
+// Loads of four floats: rows must start on 16-byte boundaries.
+bool fp32_vectors(const void* hidden, const void* weight, int H) {
+  return H % 4 == 0 && aligned16(hidden) && aligned16(weight);
+}
+
 template <int kRows>
 cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishArgs& a,
                            float4* part, int* count, TopEntry* lists, cudaStream_t st) {
   static_assert(2 * (kSimtMaxH + kScoreCols) * sizeof(float) <= kScoreSimtSmem, "two rows fit");
   const auto k =
-      a.H % 4 == 0 ? score_simt_kernel<kRows, kScoreCols, 4> : score_simt_kernel<kRows, kScoreCols, 1>;
+      fp32_vectors(hidden, weight, a.H) ? score_simt_kernel<kRows, kScoreCols, 4>
+                                        : score_simt_kernel<kRows, kScoreCols, 1>;
   const cudaError_t e = set_smem_attr(k, kScoreSimtSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.slots), static_cast<unsigned>((a.N + kRows - 1) / kRows));
@@ -309,7 +315,8 @@ cudaError_t run_score_simt(const void* hidden, const void* weight, const FinishA
 template <int kTiles>
 cudaError_t run_score_tile(const void* hidden, const void* weight, const FinishArgs& a,
                            float4* part, int* count, TopEntry* lists, cudaStream_t st) {
-  const auto k = a.H % 4 == 0 ? score_tile_kernel<kTiles, 4> : score_tile_kernel<kTiles, 1>;
+  const auto k = fp32_vectors(hidden, weight, a.H) ? score_tile_kernel<kTiles, 4>
+                                                   : score_tile_kernel<kTiles, 1>;
   const cudaError_t e = set_smem_attr(k, kTileSmem<kTiles>);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.slots),

@@ -169,3 +169,14 @@ def test_lists_of_many_rows_share_memory(lib):
     assert ws(131072, 4096, 262144, 0, 32) < 3 << 29
     assert ws(1 << 20, 512, 131072, 0, 8) < 3 << 30   # (1 GiB of hidden rows in one chunk)
     assert ws(131070, 4096, 131072, 1, 32) % 256 == 0
+
+
+def test_alignment_refusals_by_type(lib):
+    """bf16 rows go through TMA; fp32 ones may start on any element."""
+    for off in (2, 4, 8):
+        assert _fwd(lib, weight=FAKE + off) == ARG and _fwd(lib, hidden=FAKE + off) == ARG
+    for off in (1, 2, 6):
+        assert _fwd(lib, weight=FAKE + off, dtype=1) == ARG
+        assert _fwd(lib, hidden=FAKE + off, dtype=1) == ARG
+    # (past the alignment, the next check answers)
+    assert _fwd(lib, hidden=FAKE + 4, dtype=1, ws_size=256) == WS
