@@ -731,9 +731,14 @@ __device__ __forceinline__ float seen_logit(float z, float softcap) {
 template <bool kRowGrads>
 __device__ __forceinline__ float simt_logit(const float* a, const float* b, int H) {
   if constexpr (kRowGrads) {
-    double z = 0.0;
-    for (int k = 0; k < H; ++k) z = fma(static_cast<double>(a[k]), static_cast<double>(b[k]), z);
-    return static_cast<float>(z);
+    double z[4] = {0.0, 0.0, 0.0, 0.0};  // (one chain of double additions waits for each)
+    int k = 0;
+    for (; k + 4 <= H; k += 4)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        z[i] = fma(static_cast<double>(a[k + i]), static_cast<double>(b[k + i]), z[i]);
+    for (; k < H; ++k) z[0] = fma(static_cast<double>(a[k]), static_cast<double>(b[k]), z[0]);
+    return static_cast<float>((z[0] + z[1]) + (z[2] + z[3]));
   } else {
     float z = 0.f;
     for (int k = 0; k < H; ++k) z = fmaf(a[k], b[k], z);
