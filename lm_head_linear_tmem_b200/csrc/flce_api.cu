@@ -626,12 +626,16 @@ cudaError_t order_rows(const int64_t* labels, int n, int64_t V, int64_t ignore_i
   });
 }
 
+// Rows up to which one block puts the valid ones first: one launch instead of three (forward of the
+// loss at 1024 x 256 x 500: 31 against 33 us, 3001 rows 35 / 35, 4096 37 / 35, 16384 58 / 44).
+constexpr int kCompactOneBlock = 2048;
+
 // The valid rows first, in row order (the forward's and the scoring operator's
 // compaction): perm, labels_c and *n_valid.
 cudaError_t compact_rows(const int64_t* labels, int n, int64_t V, int64_t ignore_index, int* perm,
                          int64_t* labels_c, int* block_valid, long long* n_valid,
                          unsigned int* status, cudaStream_t st) {
-  if (n <= kSortMost)
+  if (n <= kCompactOneBlock)
     return order_rows(labels, n, V, ignore_index, false, nullptr, perm, labels_c, nullptr, n_valid,
                       status, st);
   const int cblk = (n + kCompactThreads - 1) / kCompactThreads;
