@@ -44,9 +44,19 @@ struct ScorePlan {
 // memory) x 64 columns (8 x 1000 x 8009: 29 us, and 55 with 256, for which most SMs get no
 // block; 8 x 4096 x 131072: 0.873 and 0.879 ms).
 constexpr int kScoreRows = 8, kScoreCols = 64;
-// More rows than this are score_tile's: 16 x 4096 x 32000 takes 0.45 ms by score_simt, and
-// 0.55 by tiles of 64 rows (24 rows: 0.86 against 0.55; 24 x 1000 x 8009: 49 against 51 us).
-constexpr int kTileFrom = 16;
+constexpr size_t kScoreSimtSmem = 200 * 1024;
+size_t score_simt_smem(int rows, int64_t H) {
+  return sizeof(float) * static_cast<size_t>(rows) * (static_cast<size_t>(H) + kScoreCols);
+}
+// Rows that are score_simt's; more are score_tile's.  24, or 16 where one block of eight rows fills
+// an SM's shared memory (H > 3536, where its loads and products take turns) and where H < 512 makes
+// neither long.  V = 32000, 24 rows, score_simt / score_tile: H = 512 68 / 88 us, 1000 140 / 152,
+// 2048 224 / 275, 3500 440 / 454; but 3584 583 / 462, 4096 663 / 522, and 256 x 8009 24 / 20.  25 rows
+// (a fourth group of eight): 2048 260 / 275, 2048 x 131072 1023 / 948, 3500 523 / 454.
+int simt_rows(int64_t H) {
+  constexpr size_t kSmSmem = 228 * 1024, kBlockOwn = 1024;  // of an SM, and what a block adds
+  return H >= 512 && 2 * (score_simt_smem(kScoreRows, H) + kBlockOwn) <= kSmSmem ? 24 : 16;
+}
 // Column tiles of a block: 1, or kWideTiles where that still leaves kWideFrom blocks for every
 // SM, which means longer lists but fewer of them (4096 x 1000 x 32000, K = 12: 9.7 ms
 // with 1, 9.0 with 4; 500 x 1000 x 10007: 0.39 with 1, 0.48 with 4).
@@ -54,10 +64,12 @@ constexpr int kWideTiles = 4, kWideFrom = 8;
 
 // Tiles of 256 columns, whose epilogue runs beside the next tile's MMAs, where a
 // 512-column tile would expose a long one: with softcap (777 x 3584 x 256000: 1.06 against 1.11
-// ms), and with alternatives over short K loops (top 8, 8192 x 2048 x 32000: 0.83 against
-// 0.93 ms; top 4, 1024 x 2048 x 131072: 0.46 against 0.54).  Else as the forward's, 512
-// (top 4, 300 x 4096 x 131072: 0.36 against 0.38 ms; none, 8192 x 2048 x 32000: 0.72
-// against 0.76).
+// ms), and with alternatives over short K loops.  There, 256 / 512 columns in turn on one box: top 8,
+// 8192 x 1024 x 32000 541 / 595 us, 8192 x 2048 x 32000 833 / 945; top 4, 1024 x 2048 x 131072
+// 430 / 486; top 20, 1000 x 2048 x 32000 131 / 202, but top 8, 4096 x 1024 x 131072 1007 / 1002 and top
+// 20, 4096 x 2048 x 131072 1896 / 1896; top 4, 4096 x 2560 x 65536 1066 / 1117.  Else as the forward's,
+// 512 (top 4, 300 x 4096 x 131072: 0.36 against 0.38 ms; none, 8192 x 2048 x 32000: 0.72 against
+// 0.76).
 constexpr int64_t kShortH = 2048;
 
 ScorePlan rows_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, int top_k,
@@ -66,7 +78,7 @@ ScorePlan rows_plan(const Opts& o, int64_t N, int64_t H, int64_t V, bool bf16, i
   P.rows = N;
   P.K = static_cast<int>(std::min<int64_t>(top_k > 0 ? top_k + kTopMargin : kPlainList, V));
   P.cap = bf16 ? top_list_cap(P.K) : P.K;
-  if (!bf16 && N > kTileFrom) {
+  if (!bf16 && N > simt_rows(H)) {
     const int64_t blocks = (N + kTileRows - 1) / kTileRows * ((V + kWideTiles * kTileCols - 1) /
                                                               (kWideTiles * kTileCols));
     P.tiles = blocks >= kWideFrom * kPlanSms ? kWideTiles : 1;
@@ -283,11 +295,6 @@ flce_status score_bf16(DevInfo* d, Opts o, const ScorePlan& P, const ScoreLayout
   e = fin.softcap > 0.f ? score(ScoreEpi<true>{}) : score(ScoreEpi<false>{});
   if (e == cudaSuccess) e = run_finish<__nv_bfloat16>(hidden, weight, fin, st);
   return e == cudaSuccess ? FLCE_OK : cuda_fail(e);
-}
-
-constexpr size_t kScoreSimtSmem = 200 * 1024;
-size_t score_simt_smem(int rows, int64_t H) {
-  return sizeof(float) * static_cast<size_t>(rows) * (static_cast<size_t>(H) + kScoreCols);
 }
 
 // Loads of four floats: rows must start on 16-byte boundaries.
