@@ -429,7 +429,6 @@ struct ScoreEpi {
 // warp per row reduces them.
 constexpr int kScoreThreads = 256;
 
-
 // Sums of n values over the 2 * o lanes that differ in the bits below 2 * o, halving the
 // values that a lane holds at each step (31 shuffles for 32 values, where a sum of its
 // own for each takes 160): lane l of 32 ends with value l / (32 / n) in v[0].
@@ -806,8 +805,8 @@ struct FinishArgs {
   float* logprobs;   // [N]; null without tokens
   float* entropy;    // [N]
   float* lse;        // [N]
-  // of the logits that the backward sees, saved_rows numbers saved_stride apart.  3: their maximum, log2 of
-  // their sum s and the entropy; 2: lse and the entropy
+  // of the logits that the backward sees, saved_rows numbers saved_stride apart.  3: their
+  // maximum, log2 of their sum s and the entropy; 2: lse and the entropy
   float* saved;
   int saved_rows, saved_stride;
   float* top_logprobs;  // [N, top_k]

@@ -116,13 +116,13 @@ constexpr float kLowExp2 = -200.0f;
 // Logits at or below this count as -inf: masked columns, whether a mask wrote -inf or
 // the type's lowest value.
 constexpr float kNoMax = -1e30f;
-// The running maximum that nothing has been merged into, a logit as well: above every
-// masked one, so that those are far below it, and finite, so that the difference of two
+// The running maximum that nothing has been merged into, a logit as well: the float above every
+// masked one, so that those are 7e22 and more below it, and finite, so that the difference of two
 // maxima is never inf - inf.
-constexpr float kNoneYet = 0.5f * kNoMax;
-// Where the temperature is so large (above 1.4e27) that even such a difference times `scale`
+constexpr float kNoneYet = -0x1.93e5920000000p+99f;
+// Where the temperature is so large (above 1.4e20) that even such a difference times `scale`
 // would not be a probability of 0, masked logits are made -inf first.
-constexpr float kTinyScale = 1e-27f;
+constexpr float kTinyScale = 1e-20f;
 
 // A softcapped logit, tanh_z = tanh(z / softcap): a product of its own, which the compiler may
 // not join with the difference that follows (an unrounded L would not equal its maximum).

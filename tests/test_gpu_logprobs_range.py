@@ -126,3 +126,22 @@ def test_masks_at_any_temperature(dtype, N, low, T):
     assert np.array_equal(ids[others], f["top_ids"]) and np.all(ids[others, 4:] == -1)
     assert torch.isneginf(got.lse[2]) and torch.all(got.top_ids[2] == -1)
     assert torch.isnan(got.logprobs[2]) and torch.isnan(got.entropy[2])
+
+
+@pytest.mark.parametrize("T", [1e-3, 1.5, 1e21])
+@pytest.mark.parametrize("dtype,N", [("bf16", 6), ("bf16", 200), ("fp32", 6), ("fp32", 70)])
+def test_logits_just_above_the_masks_count(dtype, N, T):
+    """-9.9e29 and -6e29 are logits (and far from one another); masks begin at -1e30."""
+    V = 300
+    h = np.zeros((N, 8), np.float32)
+    h[:, 0] = 1.0
+    w = np.zeros((V, 8), np.float32)
+    w[:, 0] = -9.9e29 if T < 1e21 else -1.1e30
+    w[[5, 99], 0] = -6e29
+    host, dev = on_gpu(h, w, np.full(N, 99), dtype)
+    got = flce.logprobs_forward(*dev, top_k=3, temperature=T, check_status=True)
+    assert torch.all(got.top_ids[:, 0] == 5) and torch.all(got.top_ids[:, 1] == 99)
+    assert torch.all(got.top_ids[:, 2] == (0 if T < 1e21 else -1))
+    for t in (got.logprobs, got.top_logprobs[:, 0]):
+        assert float((t + np.log(2.0)).abs().max()) <= 2.0 ** -20
+    assert float((got.entropy - np.log(2.0)).abs().max()) <= 2.0 ** -20
