@@ -393,8 +393,11 @@ struct ScoreEpi {
         for (int j = 0; j < 128; ++j)
           if (j >= ncols) r[j / 32][j % 32] = __float_as_uint(-CUDART_INF_F);
       }
-      // the cap keeps the order: the capped maximum is the maximum's cap (-inf: no columns)
-      mx_all = ncols > 0 ? cap(mx_all) : -CUDART_INF_F;
+      // (rounded tanh may swap logits a step apart, and over a tiny temperature a step is much: the
+      // maximum is that of the capped ones; -inf: no columns)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = max32(r[c]);
+      mx_all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
     }
     Stats& st = S.st;
     const float m1 = fmaxf(st.m, mx_all);  // a NaN maximum (all NaN) leaves st.m

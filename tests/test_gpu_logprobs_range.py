@@ -145,3 +145,38 @@ def test_logits_just_above_the_masks_count(dtype, N, T):
     for t in (got.logprobs, got.top_logprobs[:, 0]):
         assert float((t + np.log(2.0)).abs().max()) <= 2.0 ** -20
     assert float((got.entropy - np.log(2.0)).abs().max()) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("softcap", [17.0, 30.0, 50.0])
+@pytest.mark.parametrize("T", [1e-30, 1e-9, 1e-6])
+@pytest.mark.parametrize("dtype,N", [("bf16", 5), ("bf16", 200), ("fp32", 5), ("fp32", 40)])
+def test_softcapped_logits_one_float_apart(dtype, N, T, softcap):
+    """Consecutive floats, whose rounded tanh need not keep their order: the largest term is
+    still the largest.  The listed logits are fp64's, so the best token's is known."""
+    V = 1000
+    h = np.zeros((N, 8), np.float32)
+    h[:, :3] = 1.0
+    k = np.random.default_rng(43).permutation(V)
+    w = np.zeros((V, 8), np.float32)
+    w[:, 0] = 16.0
+    w[:, 1] = (k // 32) * 2.0 ** -14  # 16 + k 2^-19: five bits each, exact in bf16
+    w[:, 2] = (k % 32) * 2.0 ** -19
+    best = int(k.argmax())
+    host, dev = on_gpu(h, w, np.full(N, best), dtype)
+    a = torch.ones(N, device="cuda")
+    f = flce.logprobs_forward(*dev, softcap=softcap, temperature=T, top_k=2, check_status=True)
+    assert torch.all(f.top_ids[:, 0] == best)
+    r = ref.forward(h[:1], w, host[2][:1], IGN, softcap, T, 2)
+    for t in f[:4]:
+        assert torch.isfinite(t).all()
+    # (the unlisted ones are at fp32's mercy at 1e-6, where a step of L is 1 to 2 nats: within V of them)
+    assert torch.all(f.logprobs <= 2.0 ** -20) and torch.all(f.logprobs >= -np.log(2.0 * V))
+    assert torch.all(f.entropy >= -2.0 ** -20) and torch.all(f.entropy <= np.log(2.0 * V))
+    if T <= 1e-9:  # the best one has it all
+        assert float((f.lse.double() - float(r["lse"][0])).abs().max()) <= 2.0 ** -22 * abs(r["lse"][0])
+    dh, dw = flce.logprobs_backward(*dev, f.saved, a, a, softcap=softcap, temperature=T,
+                                    check_status=True)
+    # |dZ| sums to at most 2 (|a| + |b| log V) / T a row, whichever token has the probability
+    bound = 2.0 * (1 + np.log(V)) / T
+    assert float(dh.abs().max()) <= 1.01 * bound * 16.01
+    assert float(dw.abs().max()) <= 1.01 * bound * N
