@@ -1069,9 +1069,10 @@ __global__ void __launch_bounds__(kFinishThreads)
     };
     const double Me = static_cast<double>(st.m) * a.inv_temp;  // the GEMM's maximum
     double m1 = -CUDART_INF;
-    float s_rest = 0.f, t_rest = 0.f, z_sum = 0.f, dz_sum = 0.f;
+    float s_rest = 0.f, t_rest = 0.f, z_sum = 0.f, dz_sum = 0.f, z_min = CUDART_INF_F;
     for (int c = lane; c < a.K; c += 32) {
       if (ids[c] < 0) continue;
+      z_min = fminf(z_min, za[c]);
       const float L = a.softcap > 0.f ? gemm_softcap<T>(za[c], a.softcap) : za[c];
       const float d = exp2_arg(L, st.m, a.scale);
       const float e = exp2f(d);
@@ -1084,19 +1085,38 @@ __global__ void __launch_bounds__(kFinishThreads)
     // what the listed ones leave (a NaN sum stays NaN)
     s_rest = st.s - sum(s_rest);
     t_rest = st.t - sum(t_rest);
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    // The token's own logit may not be listed and yet be the largest in fp64, among others that the
+    // GEMM's rounding put before it.  It is then taken out of the rest (by what the GEMM can have
+    // had for it: its fp64 value, but no more than the least listed one) and put back like those.
+    const bool above = ids[a.K] >= 0 && xe[a.K] > m1 && m1 > -CUDART_INF;
+    if (above) {
+      m1 = xe[a.K];
+#pragma unroll
+      for (int o = 16; o >= 1; o /= 2)
+        z_min = fminf(z_min, __shfl_xor_sync(0xffffffffu, z_min, o));
+      const float z = fminf(static_cast<float>(zx[a.K]), z_min);
+      const float d = exp2_arg(a.softcap > 0.f ? gemm_softcap<T>(z, a.softcap) : z, st.m, a.scale);
+      const float e = exp2f(d);
+      s_rest -= e;
+      t_rest = fmaf(-e, d, t_rest);
+    }
     if (s_rest < 0.f) s_rest = 0.f;
     if (t_rest > 0.f) t_rest = 0.f;
+    // those that are put back: the listed ones, and the token's
+    const int back_ids = above ? a.K + 1 : a.K;
     // The backward's logits: the same GEMM's, or, fp32, fp64 sums rounded once (simt_logit),
     // whose listed terms take the places of the fp32 sums' here too.
     Stats back = st;
     if constexpr (std::is_same_v<T, float>) {
       float m = -CUDART_INF_F, s = 0.f, e_d = 0.f;
-      for (int c = lane; c < a.K; c += 32)
+      for (int c = lane; c < back_ids; c += 32)
         if (ids[c] >= 0) m = fmaxf(m, seen_logit(static_cast<float>(zx[c]), a.softcap));
 #pragma unroll
       for (int o = 16; o >= 1; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (m == -CUDART_INF_F) m = st.m;
-      for (int c = lane; c < a.K; c += 32) {
+      for (int c = lane; c < back_ids; c += 32) {
         if (ids[c] < 0) continue;
         const float L = seen_logit(static_cast<float>(zx[c]), a.softcap);
         const float d = exp2_arg(L, m, a.scale), e = exp2f(d);
@@ -1106,10 +1126,8 @@ __global__ void __launch_bounds__(kFinishThreads)
       const float d = fminf(exp2_arg(st.m, m, a.scale), 1.f), e = exp2f(d);
       back = Stats{m, sum(s) + s_rest * e, sum(e_d) + fmaf(s_rest, d, t_rest) * e};
     }
-    // ... and with their fp64 values, at the largest of those (the row's maximum is one of
-    // them; nothing is listed of a row that is all masked, or NaN)
-#pragma unroll
-    for (int o = 16; o >= 1; o /= 2) m1 = fmax(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    // ... and with their fp64 values, at the largest of those (nothing is listed of a row that is
+    // all masked, or NaN)
     if (m1 == -CUDART_INF) m1 = Me;
     // The rest is moved to that maximum.  The share that the tensor cores' truncation took of the
     // listed logits it took, on the average, of the others too; their mean (by probability) is
@@ -1129,7 +1147,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     // difference of two maxima says nothing: the rest must not outweigh the listed ones.)
     shift = fminf(fmaxf(shift, kLowExp2), 1.f);
     float s1 = 0.f, t1 = 0.f;
-    for (int c = lane; c < a.K; c += 32) {
+    for (int c = lane; c < back_ids; c += 32) {
       if (ids[c] < 0) continue;
       const float d = fmaxf(static_cast<float>((xe[c] - m1) * log2e), kLowExp2);
       const float e = exp2f(d);

@@ -180,3 +180,25 @@ def test_softcapped_logits_one_float_apart(dtype, N, T, softcap):
     bound = 2.0 * (1 + np.log(V)) / T
     assert float(dh.abs().max()) <= 1.01 * bound * 16.01
     assert float(dw.abs().max()) <= 1.01 * bound * N
+
+
+@pytest.mark.parametrize("top_k", [0, 1])
+@pytest.mark.parametrize("dtype,N,V", [("fp32", 5, 5), ("fp32", 40, 9), ("bf16", 60, 9),
+                                       ("bf16", 300, 9)])
+def test_near_ties_with_the_token_behind_the_kept_ones(dtype, N, V, top_k):
+    """V tokens alike to fp32 rounding, fewer kept than that: whichever the token is, its term is
+    counted once.  Logits of size 10 or so that differ by some 1e-6 at most (bf16: the last
+    products of H = 2000, tensor-core rounding), so every probability is 1 / V to 1e-4."""
+    H = 257 if dtype == "fp32" else 2000
+    g = np.random.default_rng(45)
+    h = g.standard_normal((N, H)).astype(np.float32)
+    w = np.tile(0.3 / np.sqrt(H / 257) * g.standard_normal(H), (V, 1))
+    if dtype == "fp32":
+        w *= 1 + 1e-7 * g.standard_normal((V, 1))
+    else:
+        w[:, -3:] = 1e-7 * g.standard_normal((V, 3))
+    host, dev = on_gpu(h, w.astype(np.float32), g.integers(0, V, N), dtype)
+    for y in range(V):
+        f = flce.logprobs_forward(dev[0], dev[1], torch.full((N,), y, device="cuda"), top_k=top_k)
+        assert float((f.logprobs + np.log(V)).abs().max()) <= 1e-4
+        assert float((f.entropy - np.log(V)).abs().max()) <= 1e-4
