@@ -755,7 +755,10 @@ __device__ __forceinline__ float simt_dz(float z, bool hit, float lse, float sof
   if constexpr (kRowGrads) {
     L = seen_logit(z, softcap);
     const float m = rg.row_max != nullptr ? rg.row_max[row] : 0.f;
-    const float lp2 = max_nan(fmaf(L - m, rg.scale, -lse * rg.lse_unit), kLowExp2);  // log2 p
+    float lp2 = max_nan(fmaf(L - m, rg.scale, -lse * rg.lse_unit), kLowExp2);  // log2 p
+    // (a logit that was not kept may come out above the forward's fp32 maximum, by rounding; over a
+    // tiny temperature that is no probability)
+    if (lp2 > 0.f) lp2 = 0.f;
     const float a = rg.d_logprobs != nullptr ? rg.d_logprobs[row] : 0.f;
     const float b = rg.d_entropy != nullptr ? rg.d_entropy[row] : 0.f;
     const float e = rg.d_entropy != nullptr ? rg.entropy[row] : 0.f;

@@ -182,6 +182,29 @@ def test_softcapped_logits_one_float_apart(dtype, N, T, softcap):
     assert float(dw.abs().max()) <= 1.01 * bound * N
 
 
+@pytest.mark.parametrize("T", [1e-30, 1e-12, 1e-9])
+@pytest.mark.parametrize("N", [5, 40])
+def test_fp32_gradients_of_near_ties_at_low_temperatures(N, T):
+    """Many tokens within fp32's rounding of the best: which of them has the probability is
+    open, but it is at most 1."""
+    H, V = 257, 200
+    g = np.random.default_rng(44)
+    h = g.standard_normal((N, H)).astype(np.float32)
+    w = np.tile(0.3 * g.standard_normal(H), (V, 1))
+    w = (w * (1 + 1e-7 * g.standard_normal((V, 1)))).astype(np.float32)
+    host, dev = on_gpu(h, w, g.integers(0, V, N), "fp32")
+    a = torch.ones(N, device="cuda")
+    f = flce.logprobs_forward(*dev, temperature=T, check_status=True)
+    for t in f[:3]:
+        assert torch.isfinite(t).all()
+    assert torch.all(f.logprobs <= 2.0 ** -20)
+    dh, dw = flce.logprobs_backward(*dev, f.saved, a, a, temperature=T, check_status=True)
+    # each of V probabilities at most 1
+    bound = 1.01 * V * (2.0 + 2 * np.log(V)) / T
+    assert float(dh.abs().max()) <= bound * np.abs(w).max()
+    assert float(dw.abs().max()) <= bound * N * np.abs(h).max()
+
+
 @pytest.mark.parametrize("top_k", [0, 1])
 @pytest.mark.parametrize("dtype,N,V", [("fp32", 5, 5), ("fp32", 40, 9), ("bf16", 60, 9),
                                        ("bf16", 300, 9)])
