@@ -64,7 +64,7 @@ constexpr int kWideTiles = 4, kWideFrom = 8;
 
 // Tiles of 256 columns, whose epilogue runs beside the next tile's MMAs, where a
 // 512-column tile would expose a long one: with softcap (777 x 3584 x 256000: 1.06 against 1.11
-// ms), and with alternatives over short K loops.  There, 256 / 512 columns in turn on one box: top 8,
+// ms), and with alternatives over short K loops.  There, 256 / 512 columns, timed in turn: top 8,
 // 8192 x 1024 x 32000 541 / 595 us, 8192 x 2048 x 32000 833 / 945; top 4, 1024 x 2048 x 131072
 // 430 / 486; top 20, 1000 x 2048 x 32000 131 / 202, but top 8, 4096 x 1024 x 131072 1007 / 1002 and top
 // 20, 4096 x 2048 x 131072 1896 / 1896; top 4, 4096 x 2560 x 65536 1066 / 1117.  Else as the forward's,
